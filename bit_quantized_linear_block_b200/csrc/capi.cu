@@ -549,6 +549,52 @@ ql_status qlinear_quantize_act(const void* X, int64_t M, int32_t K, int32_t act_
   return launch_quant_int8_tensor_perm(X, M, K, w->Kp, w->gather, amax, codes, scales, st, qmax);
 }
 
+// ---------------------------------------------------------------- residual + norm + quantize
+ql_status qlinear_norm_quantize(const void* X, const void* residual, const void* gamma, int64_t M, int32_t K, float eps,
+                                int32_t act_fmt, int32_t hadamard, void* residual_out, void* norm_out, void* codes,
+                                float* scales, void* stream) {
+  QL_TRY(check_m(M));
+  QL_TRY(check_k(K));
+  if (K > 32768) return QL_ERR_UNSUPPORTED_SHAPE;
+  const int qmax = act_qmax(act_fmt);
+  const int32_t fmt = int_base_fmt(act_fmt);
+  if (fmt != QL_ROUTE_INT8 && fmt != QL_ACT_INT8_F16 && fmt != QL_ROUTE_BF16) return QL_ERR_INVALID_ARG;
+  const bool plain = fmt == QL_ROUTE_BF16;
+  if (!(eps > 0.f) || eps > 3.4028235e38f) return QL_ERR_INVALID_ARG;
+  if (plain && (hadamard != 0 || norm_out != nullptr)) return QL_ERR_INVALID_ARG;
+  if (residual == nullptr && residual_out != nullptr) return QL_ERR_INVALID_ARG;
+  if (M > 0 && (X == nullptr || gamma == nullptr || codes == nullptr || (!plain && scales == nullptr)))
+    return QL_ERR_INVALID_ARG;
+  if (!aligned(X, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(residual_out, 16) ||
+      !aligned(norm_out, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+    return QL_ERR_ALIGNMENT;
+  const size_t row_bytes = static_cast<size_t>(M) * K * 2;
+  struct Span {
+    const void* p;
+    size_t bytes;
+    bool in_place;   // an output that may be exactly X or residual
+  };
+  const Span in[3] = {{X, row_bytes, false}, {residual, row_bytes, false}, {gamma, static_cast<size_t>(K) * 2, false}};
+  const Span out[4] = {{residual_out, row_bytes, true},
+                       {norm_out, row_bytes, true},
+                       {codes, fmt == QL_ROUTE_INT8 ? row_bytes / 2 : row_bytes, false},
+                       {plain ? nullptr : scales, static_cast<size_t>(M) * 4, false}};
+  auto overlap = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (overlap(out[o], in[i]) && !(out[o].in_place && i < 2 && out[o].p == in[i].p)) return QL_ERR_INVALID_ARG;
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o], out[i])) return QL_ERR_INVALID_ARG;
+  }
+  QL_TRY(device_ready());
+  return launch_norm_quantize(X, residual, gamma, M, K, eps, plain ? 2 : fmt == QL_ACT_INT8_F16 ? 1 : 0,
+                              hadamard ? 1 : 0, qmax, residual_out, norm_out, codes, scales,
+                              static_cast<cudaStream_t>(stream));
+}
+
 // ---------------------------------------------------------------- GEMM
 ql_status qlinear_gemm(int32_t act_fmt, const void* a_codes, const void* a_sf, const float* a_scales,
                        int64_t M, const ql_weights* w, void* Y, void* stream) {

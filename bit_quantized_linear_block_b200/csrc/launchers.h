@@ -50,6 +50,11 @@ ql_status launch_quant_int8_token(const void* x, int64_t M, int32_t K, int hadam
 ql_status launch_quant_int8_tensor_perm(const void* x, int64_t M, int32_t K, int32_t Kp,
                                         const int32_t* gather, const float* amax_in, void* codes,
                                         float* scale_out, cudaStream_t st, int qmax = 127);
+// Residual + RMS norm + per-token quantization; out_kind: 0 int8 codes, 1 f16
+// codes, 2 the bf16 norm itself (codes).  residual, residual_out, norm_out may be null.
+ql_status launch_norm_quantize(const void* x, const void* residual, const void* gamma, int64_t M, int32_t K, float eps,
+                               int out_kind, int hadamard, int qmax, void* residual_out, void* norm_out, void* codes,
+                               float* scales, cudaStream_t st);
 ql_status launch_gamma_route(const void* in, const void* out, int64_t numel, float threshold,
                              double* gamma, int32_t* route, void* ws, cudaStream_t st);
 // sums[0] = sum |out - in|, sums[1] = sum |in| (fp64); ws as for launch_gamma_route.

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -93,6 +94,7 @@ def _load() -> C.CDLL:
         "qlinear_tensor_amax": (C.c_int, [vp, i64, i32, i32, vp, vp, sz, vp]),
         "qlinear_quantize_act": (C.c_int, [vp, i64, i32, i32, i32, C.POINTER(Weights), vp, vp, vp,
                                            vp, vp, vp, sz, vp]),
+        "qlinear_norm_quantize": (C.c_int, [vp, vp, vp, i64, i32, f32, i32, i32, vp, vp, vp, vp, vp]),
         "qlinear_gemm": (C.c_int, [i32, vp, vp, vp, i64, C.POINTER(Weights), vp, vp]),
         "qlinear_forward_ws_bytes": (sz, [i64, C.POINTER(Weights), i32]),
         "qlinear_forward": (C.c_int, [vp, i64, C.POINTER(Weights), i32, vp, vp, sz, vp]),
@@ -130,6 +132,18 @@ def _stream(stream, device):
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the call runs on {device}")
     return C.c_void_p(stream.cuda_stream)
+
+
+def _call_on(device, stream, *inputs):
+    """A context for one call on `device`: new tensors belong to the stream
+    that the call runs on, and when that is not the current stream the
+    inputs' memory is kept until the call is done with it."""
+    if stream is None:
+        return nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    return torch.cuda.stream(stream)
 
 
 def _tensor(t, name: str, dtype=None, device=None, min_bytes: int | None = None, dim: int | None = None):
@@ -431,6 +445,60 @@ def qlinear_quantize_act(X: torch.Tensor, act_fmt: int, hadamard: bool = True,
                                         _ptr(codes), _ptr(sf_mma), _ptr(sf_rm), _ptr(scales), _ptr(ws),
                                         ws.numel(), st))
     return dict(codes=codes, sf_mma=sf_mma, sf_rowmajor=sf_rm, scales=scales, _ws=ws)
+
+
+_NORM_DTYPES = {QL_ROUTE_INT8: torch.int8, QL_ROUTE_INT6: torch.int8, QL_ACT_INT8_F16: torch.float16,
+                QL_ACT_INT6_F16: torch.float16, QL_ROUTE_BF16: torch.bfloat16}
+
+
+def qlinear_norm_quantize(X: torch.Tensor, gamma: torch.Tensor, act_fmt: int = QL_ROUTE_INT8, hadamard: bool = True,
+                          residual: torch.Tensor | None = None, eps: float = 1e-6, keep_norm: bool = False,
+                          out: dict | None = None, stream=None) -> dict:
+    """Residual addition, RMS norm and per-token quantization in one pass:
+    h = X + residual, y = h / rms(h) * gamma, and y quantized as
+    qlinear_quantize_act would (act_fmt: QL_ROUTE_INT8 / INT6,
+    QL_ACT_INT8_F16 / INT6_F16; QL_ROUTE_BF16 gives y itself and takes
+    hadamard as False).  Returns qlinear_quantize_act's dict (codes, scales)
+    plus "residual" (h, None without a residual) and "norm" (y with
+    keep_norm, else None).  `out` reuses the buffers of an earlier result;
+    out["residual"] may be X or residual itself (in place)."""
+    _tensor(X, "X", torch.bfloat16, dim=2)
+    dev = X.device
+    M, K = X.shape
+    _tensor(gamma, "gamma", torch.bfloat16, dev, dim=1)
+    if gamma.numel() != K:
+        raise ValueError(f"gamma has {gamma.numel()} elements, X has {K} columns")
+    if act_fmt not in _NORM_DTYPES:
+        raise ValueError(f"activation format {act_fmt} has no per-token form")
+    if residual is not None:
+        _tensor(residual, "residual", torch.bfloat16, dev, dim=2)
+        if residual.shape != X.shape:
+            raise ValueError(f"residual {tuple(residual.shape)} and X {tuple(X.shape)} differ in shape")
+    plain = act_fmt == QL_ROUTE_BF16
+    if plain and keep_norm:
+        raise ValueError("keep_norm: QL_ROUTE_BF16 already returns the norm as its codes")
+    st = _stream(stream, dev)
+    with _call_on(dev, stream, X, gamma, residual):
+        if out is None:
+            codes = torch.empty((M, K), dtype=_NORM_DTYPES[act_fmt], device=dev)
+            scales = None if plain else torch.empty(max(M, 1), dtype=torch.float32, device=dev)
+            h = None if residual is None else torch.empty_like(X)
+            y = torch.empty_like(X) if keep_norm else None
+        else:
+            codes = _tensor(out["codes"], "out['codes']", _NORM_DTYPES[act_fmt], dev,
+                            M * K * _NORM_DTYPES[act_fmt].itemsize)
+            scales = None if plain else _tensor(out["scales"], "out['scales']", torch.float32, dev, 4 * M)
+            h = None if residual is None else out.get("residual")
+            y = out.get("norm") if keep_norm else None
+            if h is not None:
+                _tensor(h, "out['residual']", torch.bfloat16, dev, 2 * M * K)
+            if keep_norm:
+                _tensor(y, "out['norm']", torch.bfloat16, dev, 2 * M * K)
+        _check("qlinear_norm_quantize",
+               lib.qlinear_norm_quantize(_ptr(X), _ptr(residual), _ptr(gamma), M, K, eps, act_fmt,
+                                         int(bool(hadamard) and not plain), _ptr(h), _ptr(y), _ptr(codes),
+                                         _ptr(scales), st))
+    return dict(codes=codes, sf_mma=None, sf_rowmajor=None, scales=scales, residual=h, norm=y)
 
 
 def _output(Y, M: int, N: int, dev):

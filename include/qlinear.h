@@ -297,6 +297,29 @@ QL_API ql_status qlinear_quantize_act(const void* X_bf16, int64_t M, int32_t K,
                                       void* sf_rowmajor, float* scales,
                                       void* ws, size_t ws_bytes, void* stream);
 
+/* ---- residual + RMS norm + activation quantization --------------------------
+   What stands before a quantized layer in a decoder block, in one pass over
+   the rows (one launch, no workspace):
+     h = bf16(X + residual)  (h = X without a residual)
+     y = bf16(RN(RN(h rstd) gamma)),  rstd = RN(1 / sqrt(sum h^2 / K + eps))
+         with the sum in fp64
+     codes, scales = what qlinear_quantize_act gives for y in act_fmt, bit for
+         bit: QL_ROUTE_INT8, QL_ROUTE_INT6 (int8 [M, K] + fp32 [M]),
+         QL_ACT_INT8_F16, QL_ACT_INT6_F16 (f16 [M, K] + fp32 [M]); or y itself
+         for QL_ROUTE_BF16 (codes bf16 [M, K], scales unused, hadamard 0).
+   gamma: bf16 [K].  residual: bf16 [M, K] or NULL.  residual_out: h, bf16
+   [M, K], or NULL (needs a residual).  norm_out: y, bf16 [M, K], or NULL
+   (NULL for QL_ROUTE_BF16).  eps must be finite and > 0.  residual_out and
+   norm_out may be exactly X or residual (in place); every other overlap
+   between an output and an input or another output is QL_ERR_INVALID_ARG.
+   K <= 32768 (a row stays in the registers of one CTA), else
+   QL_ERR_UNSUPPORTED_SHAPE.  A row with a non-finite value gives unspecified
+   codes for that row only. */
+QL_API ql_status qlinear_norm_quantize(const void* X_bf16, const void* residual_bf16, const void* gamma_bf16,
+                                       int64_t M, int32_t K, float eps, int32_t act_fmt, int32_t hadamard,
+                                       void* residual_out, void* norm_out, void* codes, float* scales,
+                                       void* stream);
+
 /* ---- GEMM on quantized activations ----------------------------------------
    Y[m, n] = bf16(alpha_m * sum_k a[m,k] w[n,k]) with fp32 accumulation:
    QL_ROUTE_NVFP4:     tcgen05 block-scaled FP4 MMA; alpha = g_x g_w / 128 if
