@@ -638,6 +638,23 @@ ql_status qlinear_gemm(int32_t act_fmt, const void* a_codes, const void* a_sf, c
   return launch_gemm_qarvd(a_codes, a_scales, M, w, Y, st, status);
 }
 
+// ---------------------------------------------------------------- few rows
+ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_scales, int64_t M, const ql_weights* w, void* Y,
+                       void* stream) {
+  if (M < 0) return QL_ERR_INVALID_ARG;
+  if (M > 16) return QL_ERR_UNSUPPORTED_SHAPE;
+  QL_TRY(check_w(w));
+  if (w->fmt != QL_W_NVFP4) return QL_ERR_INVALID_ARG;
+  const int32_t fmt = int_base_fmt(act_fmt);
+  if (fmt != QL_ROUTE_BF16 && fmt != QL_ROUTE_INT8 && fmt != QL_ACT_INT8_F16) return QL_ERR_INVALID_ARG;
+  if (M > 0 && (a == nullptr || Y == nullptr || (fmt != QL_ROUTE_BF16 && a_scales == nullptr)))
+    return QL_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(Y, 16) || !aligned(a_scales, 4)) return QL_ERR_ALIGNMENT;
+  QL_TRY(device_ready());
+  return launch_gemv(fmt == QL_ROUTE_BF16 ? 0 : fmt == QL_ACT_INT8_F16 ? 1 : 2, a, a_scales, M, w, Y,
+                     static_cast<cudaStream_t>(stream));
+}
+
 // ---------------------------------------------------------------- forward
 size_t qlinear_forward_ws_bytes(int64_t M, const ql_weights* w, int32_t route) {
   if (M < 0 || check_w(w) != QL_OK) return 0;

@@ -1,0 +1,524 @@
+// The quantized linear layer for few rows (1 to 16) on NVFP4 weights, and the
+// same product grouped by expert when the experts have few rows each.
+//
+//   Y[m, n] = bf16(alpha_m sum_k a[m, k] (e2m1[n, k] * e4m3[n, k / 16]))
+//
+// a: integer codes (int8 or their f16 values), or bf16 rows, rotated here by
+// blockdiag(H_128) when the weights are.  alpha_m = RN(g_w alpha_mul), times
+// the row's scale for codes.
+//
+// Bound: the weights, 9/16 byte each, are read once and the rows are few, so
+// HBM (L2 for a layer that stays there) is the limit and the multiply only
+// has to keep up.  A 128-row tensor-memory tile would leave most of its
+// columns empty and pay the pipeline's fill for one K sweep; here a warp
+// streams its share of the weights straight into mma.sync fragments:
+//
+//   * unit: 64 weight rows (four 16-row MMA tiles) x one 128-element K block,
+//     9 half-KB pieces; the rows are 16 consecutive r % 32 of one 128-row
+//     scale atom and their three 32-row shifts, so that one 16-byte load of
+//     scales serves the four tiles;
+//   * a CTA (W warps) owns 64 rows, its warps the K blocks of its K range in
+//     turn; a cluster of S CTAs splits K further when the rows alone do not
+//     fill the GPU.  Partial sums are added in a fixed order (warps through
+//     shared memory, CTAs through distributed shared memory), so results do
+//     not depend on timing and need no workspace;
+//   * each lane copies the pieces it will read itself (cp.async, kDepth
+//     blocks ahead), so the ring needs no barrier.
+//
+// MMA operands are f16: a weight value E2M1 x E4M3 (at most 6 significant
+// bits, 2^-10 .. 2688) and an integer code are exact, products and sums are
+// fp32.  A bf16 row block (rotated or not) is scaled by a power of two that
+// brings its largest magnitude into [2^14, 2^15) and rounded to f16: 11
+// significant bits against the 8 of the bf16 output, and exact for an
+// unrotated block's bf16 values down to 2^-29 of its largest; the block's
+// sums are scaled back in fp32.
+#include "ql_common.cuh"
+#include "gemm_common.cuh"
+#include "launchers.h"
+
+namespace ql {
+
+namespace {
+
+constexpr int kGvRows = 64;                 // weight rows per CTA
+constexpr int kGvMaxWarps = 8;
+constexpr int kGvDepth = 2;                 // K blocks in flight per warp
+constexpr int kGvCodeBytes = 8 * 512;       // 4 MMA tiles x 2 row halves x 32 lanes x 16 bytes
+constexpr int kGvStage = kGvCodeBytes + 2 * 512;   // + the scales of both row halves
+constexpr int kGvMaxCluster = 8;
+
+enum GvAct { kGvBf16 = 0, kGvF16 = 1, kGvI8 = 2 };
+
+struct GvArgs {
+  const uint8_t* a;          // rows [rows_a, K]
+  const float* a_scales;     // fp32 [rows_a] (codes)
+  const uint8_t* codes;      // [N, K/2], of expert e at + e * expert_codes
+  const uint8_t* sf;         // MMA layout, of expert e at + e * expert_sf
+  const float* gscale;       // [E]
+  __nv_bfloat16* y;          // [rows, N]
+  const int32_t* offsets;    // grouped: [E + 1]
+  const int32_t* rows;       // grouped: source row of each output row, or null
+  int64_t rows_a, rows_y;
+  size_t expert_codes, expert_sf;
+  int32_t M, N, K, E;
+  int32_t hadamard, cluster;
+  float alpha_mul;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+// D (16 x 8, fp32) += A (16 x 16, f16) B (16 x 8, f16)
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t h2_bits(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+__device__ __forceinline__ __half2 bits_h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+
+// Eight E2M1 codes -> four f16x2 words of their values (hardware convert).
+__device__ __forceinline__ void fp4x8_to_f16(uint32_t codes, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+      "mov.b32 {c0, c1, c2, c3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, c0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, c1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, c3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+}
+
+// int8 x4 -> two f16x2 words of the exact values (a byte permute builds
+// 1024 + (q + 128) in f16, a packed subtract removes the offset).
+__device__ __forceinline__ void i8x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 off = bits_h2(0x64806480u);   // 1152
+  lo = h2_bits(__hsub2(bits_h2(__byte_perm(u, 0x64646464u, 0x4140u)), off));
+  hi = h2_bits(__hsub2(bits_h2(__byte_perm(u, 0x64646464u, 0x4342u)), off));
+}
+
+// This lane's 32 elements [32 t, 32 t + 32) of a 128-element block as 16
+// f16x2 words, t = lane % 4; for bf16 rows also the factor that undoes the
+// block's power-of-two scaling.  All lanes of the warp call it.
+template <int ACT>
+__device__ __forceinline__ float block_to_f16(const uint4 (&raw)[4], int hadamard, uint32_t (&w)[16]) {
+  if constexpr (ACT == kGvF16) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      w[4 * q] = raw[q].x;
+      w[4 * q + 1] = raw[q].y;
+      w[4 * q + 2] = raw[q].z;
+      w[4 * q + 3] = raw[q].w;
+    }
+    return 1.f;
+  } else if constexpr (ACT == kGvI8) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      i8x4_to_f16x4(raw[q].x, w[8 * q], w[8 * q + 1]);
+      i8x4_to_f16x4(raw[q].y, w[8 * q + 2], w[8 * q + 3]);
+      i8x4_to_f16x4(raw[q].z, w[8 * q + 4], w[8 * q + 5]);
+      i8x4_to_f16x4(raw[q].w, w[8 * q + 6], w[8 * q + 7]);
+    }
+    return 1.f;
+  } else {
+    float2 P[16];   // (x_j, x_{j + 16})
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t lo[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+      const uint32_t hi[4] = {raw[q + 2].x, raw[q + 2].y, raw[q + 2].z, raw[q + 2].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        P[8 * q + 2 * i] = make_float2(bf16_lo(lo[i]), bf16_lo(hi[i]));
+        P[8 * q + 2 * i + 1] = make_float2(bf16_hi(lo[i]), bf16_hi(hi[i]));
+      }
+    }
+    if (hadamard) {   // distances 1..8 between pairs, 16 inside a pair, 32 and 64 across lanes
+      const float2 m1 = make_float2(-1.f, -1.f);
+#pragma unroll
+      for (int s = 1; s < 16; s <<= 1) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if ((j & s) == 0) {
+            const float2 a = P[j], b = P[j + s];
+            P[j] = __fadd2_rn(a, b);
+            P[j + s] = __ffma2_rn(b, m1, a);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) P[j] = make_float2(__fadd_rn(P[j].x, P[j].y), __fsub_rn(P[j].x, P[j].y));
+#pragma unroll
+      for (int s = 1; s < 4; s <<= 1) {
+        const float sg = (lane_id() & s) ? -1.f : 1.f;
+        const float2 sg2 = make_float2(sg, sg);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float2 o;
+          o.x = __shfl_xor_sync(0xffffffffu, P[j].x, s);
+          o.y = __shfl_xor_sync(0xffffffffu, P[j].y, s);
+          P[j] = __ffma2_rn(P[j], sg2, o);
+        }
+      }
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = fmax3(m, fabsf(P[j].x), fabsf(P[j].y));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // 2^(141 - e) brings [2^(e - 127), 2^(e - 126)) to [2^14, 2^15); e >= 15
+    // keeps it and its inverse normal numbers (a smaller block only loses
+    // bits far below the fp32 sums)
+    const uint32_t e = max(__float_as_uint(m) >> 23, 15u);
+    const float mul = __uint_as_float((268u - e) << 23);
+    const float2 mul2 = make_float2(mul, mul);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) P[j] = __fmul2_rn(P[j], mul2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[i] = h2_bits(__floats2half2_rn(P[2 * i].x, P[2 * i + 1].x));
+      w[8 + i] = h2_bits(__floats2half2_rn(P[2 * i].y, P[2 * i + 1].y));
+    }
+    return __uint_as_float((e - 14u) << 23);
+  }
+}
+
+}  // namespace
+
+// NT: tiles of 8 rows of `a` (1: up to 8 rows, 2: up to 16).
+template <int NT, int ACT, bool GROUPED>
+__global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(const GvArgs p) {
+  constexpr int kTokens = 8 * NT;
+  constexpr bool kScaled = ACT == kGvBf16;       // a factor per row and K block
+  constexpr int kRaw = ACT == kGvI8 ? 2 : 4;     // 16-byte pieces of a lane's 32 elements
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+  const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
+  const int S = p.cluster;
+  const int unit = blockIdx.x / S, rank = blockIdx.x - unit * S;
+  pdl_wait();
+
+  int M = p.M;
+  int64_t row0 = 0;
+  const uint8_t* codes = p.codes;
+  const uint8_t* sf = p.sf;
+  const float* gscale = p.gscale;
+  if constexpr (GROUPED) {
+    // blockIdx.y counts the row tiles of all experts in order
+    int tile = blockIdx.y, e0 = 0;
+    bool found = false;
+    for (; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int64_t lo = 0;
+      int cnt = 0;
+      if (e < p.E) {
+        lo = min(max(static_cast<int64_t>(p.offsets[e]), int64_t(0)), p.rows_y);
+        cnt = static_cast<int>(min(max(static_cast<int64_t>(p.offsets[e + 1]), lo), p.rows_y) - lo);
+      }
+      const int tiles = (cnt + kTokens - 1) / kTokens;
+      int end = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, tile < end);
+      if (hit != 0) {
+        const int src = __ffs(hit) - 1;
+        const int first = __shfl_sync(0xffffffffu, end - tiles, src);
+        const int c = __shfl_sync(0xffffffffu, cnt, src);
+        row0 = __shfl_sync(0xffffffffu, lo, src) + static_cast<int64_t>(tile - first) * kTokens;
+        M = min(kTokens, c - (tile - first) * kTokens);
+        e0 += src;
+        found = true;
+        break;
+      }
+      tile -= __shfl_sync(0xffffffffu, end, 31);
+    }
+    if (!found) {                                // past the last tile: the same for the whole cluster
+      pdl_release();
+      return;
+    }
+    codes += static_cast<size_t>(e0) * p.expert_codes;
+    sf += static_cast<size_t>(e0) * p.expert_sf;
+    gscale += e0;
+  }
+
+  // 64 weight rows of this CTA: tile i holds rows first + 32 i .. + 15
+  const int first = 128 * (unit >> 1) + 16 * (unit & 1);
+  const int ntiles = min(4, (p.N - first + 31) / 32);          // tiles inside N (N and the tiles are 16-aligned)
+  const int kb_all = p.K >> 7;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(kb_all) * rank / S);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(kb_all) * (rank + 1) / S);
+  const int nblk = max(0, (kb1 - kb0 - warp + warps - 1) / warps);   // blocks kb0 + warp + j * warps
+  const size_t row_bytes = static_cast<size_t>(p.K) / 2;
+  const uint8_t* wsrc = codes + static_cast<size_t>(first + g) * row_bytes + 16 * t;
+  const uint8_t* ssrc = sf + (static_cast<size_t>(unit >> 1) * (p.K >> 6) + (t >> 1)) * 512 +
+                        static_cast<size_t>(16 * (unit & 1) + g) * 16;
+  uint8_t* ring = smem + warp * (kGvDepth * kGvStage);
+  uint8_t* xbuf = smem + warps * (kGvDepth * kGvStage) + warp * (NT * 2048 + NT * 32);
+  float* xscale = reinterpret_cast<float*>(xbuf + NT * 2048);
+  auto issue = [&](int j) {                      // weights and scales of block j into its ring slot
+    if (j < nblk) {
+      const int kb = kb0 + warp + j * warps;
+      const uint32_t dst = smem_u32(ring + (j % kGvDepth) * kGvStage) + 16 * lane;
+      for (int i = 0; i < ntiles; ++i) {
+        const uint8_t* src = wsrc + static_cast<size_t>(32 * i) * row_bytes + static_cast<size_t>(kb) * 64;
+        cp_async16(dst + (2 * i) * 512, src);
+        cp_async16(dst + (2 * i + 1) * 512, src + 8 * row_bytes);
+      }
+      const uint8_t* s = ssrc + static_cast<size_t>(kb) * 1024;
+      cp_async16(dst + kGvCodeBytes, s);
+      cp_async16(dst + kGvCodeBytes + 512, s + 128);
+    }
+    cp_async_commit();                           // a group per block, empty past the end
+  };
+#pragma unroll
+  for (int j = 0; j < kGvDepth; ++j) issue(j);
+
+  // Rows of `a`: lane group g (four lanes) converts one (block, row) pair of a
+  // batch of `gb` blocks x `m2` rows, gb m2 = 8 (NT = 2: one block, 8 rows twice).
+  const int m2 = NT == 2 ? 8 : M > 4 ? 8 : M > 2 ? 4 : M;
+  const int gb = 8 / m2;
+  const int pair_blk = g / m2, pair_row = g - pair_blk * m2;
+  const uint8_t* asrc[NT];
+  bool a_ok[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int m = 8 * nt + pair_row;
+    int64_t src = row0 + m;
+    a_ok[nt] = m < M;
+    if (GROUPED && p.rows != nullptr && a_ok[nt]) src = p.rows[row0 + m];
+    a_ok[nt] = a_ok[nt] && src >= 0 && src < p.rows_a;
+    asrc[nt] = p.a + (static_cast<size_t>(a_ok[nt] ? src : 0) * p.K + 32 * t) * (ACT == kGvI8 ? 1 : 2);
+  }
+  uint4 raw[NT][4];
+  auto load_a = [&](int j0) {
+    const int j = j0 + pair_blk;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint8_t* src = asrc[nt] + static_cast<size_t>(kb0 + warp + j * warps) * (ACT == kGvI8 ? 128 : 256);
+#pragma unroll
+      for (int q = 0; q < kRaw; ++q)
+        raw[nt][q] = (a_ok[nt] && j < nblk) ? *reinterpret_cast<const uint4*>(src + 16 * q) : make_uint4(0, 0, 0, 0);
+    }
+  };
+
+  float acc[4][NT][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.f;
+
+  if (nblk > 0) load_a(0);
+  for (int j0 = 0; j0 < nblk; j0 += gb) {
+    __syncwarp();                                // the previous batch has been read
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      uint32_t w[16];
+      const float f = block_to_f16<ACT>(raw[nt], p.hadamard, w);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(xbuf + nt * 2048 + q * 512 + lane * 16) =
+            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      if (kScaled && t == 0) xscale[8 * nt + g] = f;
+    }
+    __syncwarp();
+    if (j0 + gb < nblk) load_a(j0 + gb);
+    const int batch = min(gb, nblk - j0);
+    for (int b = 0; b < batch; ++b) {
+      const int j = j0 + b;
+      cp_async_wait<kGvDepth - 1>();             // this lane's own pieces of block j have landed
+      const uint8_t* slot = ring + (j % kGvDepth) * kGvStage + 16 * lane;
+      uint4 xf[NT][4];                           // B fragments: row g of the tile, elements 32 t + 8 q ..
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          xf[nt][q] = g < m2 ? lds128(xbuf + nt * 2048 + q * 512 + (b * m2 * 4 + lane) * 16)
+                             : make_uint4(0, 0, 0, 0);
+      const uint4 sa = lds128(slot + kGvCodeBytes), sb = lds128(slot + kGvCodeBytes + 512);
+      const uint32_t sa4[4] = {sa.x, sa.y, sa.z, sa.w}, sb4[4] = {sb.x, sb.y, sb.z, sb.w};
+      float f0[NT], f1[NT];
+      if constexpr (kScaled) {                   // factors of rows 2t and 2t + 1 (columns of the accumulator)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          f0[nt] = xscale[8 * nt + min(b * m2 + 2 * t, 7)];
+          f1[nt] = xscale[8 * nt + min(b * m2 + 2 * t + 1, 7)];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= ntiles) break;                  // warp-uniform
+        const uint4 ca = lds128(slot + (2 * i) * 512), cb = lds128(slot + (2 * i + 1) * 512);
+        const uint32_t ca4[4] = {ca.x, ca.y, ca.z, ca.w}, cb4[4] = {cb.x, cb.y, cb.z, cb.w};
+        // the two block scales of elements 32 t .. 32 t + 31, as f16 pairs
+        uint32_t s2a, s2b;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2a) : "h"(static_cast<uint16_t>(sa4[i] >> (16 * (t & 1)))));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2b) : "h"(static_cast<uint16_t>(sb4[i] >> (16 * (t & 1)))));
+        const __half2 va[2] = {__low2half2(bits_h2(s2a)), __high2half2(bits_h2(s2a))};
+        const __half2 vb[2] = {__low2half2(bits_h2(s2b)), __high2half2(bits_h2(s2b))};
+        float part[NT][4];
+        if constexpr (kScaled) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) part[nt][c] = 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t ha[4], hb[4];
+          fp4x8_to_f16(ca4[q], ha);
+          fp4x8_to_f16(cb4[q], hb);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            ha[c] = h2_bits(__hmul2(bits_h2(ha[c]), va[q >> 1]));
+            hb[c] = h2_bits(__hmul2(bits_h2(hb[c]), vb[q >> 1]));
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float (&d)[4] = kScaled ? part[nt] : acc[i][nt];
+            mma_f16(d, ha[0], hb[0], ha[1], hb[1], xf[nt][q].x, xf[nt][q].y);
+            mma_f16(d, ha[2], hb[2], ha[3], hb[3], xf[nt][q].z, xf[nt][q].w);
+          }
+        }
+        if constexpr (kScaled) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            acc[i][nt][0] = fmaf(part[nt][0], f0[nt], acc[i][nt][0]);
+            acc[i][nt][1] = fmaf(part[nt][1], f1[nt], acc[i][nt][1]);
+            acc[i][nt][2] = fmaf(part[nt][2], f0[nt], acc[i][nt][2]);
+            acc[i][nt][3] = fmaf(part[nt][3], f1[nt], acc[i][nt][3]);
+          }
+        }
+      }
+      issue(j + kGvDepth);                       // the slot just read
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();                               // the ring is free: it becomes the reduction buffer
+
+  // acc[i][nt][c]: weight row 16 i + g + 8 (c / 2) of the unit, row 8 nt + 2 t + c % 2 of a
+  constexpr int kPitch = kGvRows + 1;
+  float* red = reinterpret_cast<float*>(smem);   // [warps][kTokens][kPitch], then [kTokens][kPitch] sums
+  float* sum = red + warps * kTokens * kPitch;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        red[(warp * kTokens + 8 * nt + 2 * t + (c & 1)) * kPitch + 16 * i + g + 8 * (c >> 1)] = acc[i][nt][c];
+  __syncthreads();
+  for (int o = threadIdx.x; o < M * kGvRows; o += blockDim.x) {
+    const int m = o >> 6, r = o & 63;
+    float v = 0.f;
+    for (int w = 0; w < warps; ++w) v += red[(w * kTokens + m) * kPitch + r];
+    sum[m * kPitch + r] = v;
+  }
+  __syncwarp();
+  if (S > 1) cluster_sync();
+  else __syncthreads();
+  const float alpha = __fmul_rn(ld_dep(gscale), p.alpha_mul);
+  // the cluster's CTAs share the unit's outputs
+  for (int o = rank * blockDim.x + threadIdx.x; o < M * kGvRows; o += S * blockDim.x) {
+    const int m = o >> 6, r = o & 63;
+    const int n = first + 32 * (r >> 4) + (r & 15);
+    float v = 0.f;
+    if (S > 1) {
+      const uint32_t addr = smem_u32(sum + m * kPitch + r);
+      for (int c = 0; c < S; ++c) v += ld_cluster_f32(map_to_rank(addr, c));
+    } else {
+      v = sum[m * kPitch + r];
+    }
+    if (n < p.N) {
+      float a = alpha;
+      if constexpr (ACT != kGvBf16) {
+        int64_t src = row0 + m;
+        if (GROUPED && p.rows != nullptr) src = p.rows[row0 + m];
+        a = src >= 0 && src < p.rows_a ? __fmul_rn(alpha, ld_dep(p.a_scales + src)) : 0.f;
+      }
+      p.y[(row0 + m) * p.N + n] = __float2bfloat16_rn(__fmul_rn(a, v));
+    }
+  }
+  pdl_release();
+  __syncwarp();
+  if (S > 1) cluster_sync();                     // no CTA leaves while another reads its sums
+}
+
+namespace {
+
+// 64-row units with at least one 16-row tile inside N.
+int gemv_units(int32_t N) {
+  const int r = N % 128;
+  return 2 * (N / 128) + (r == 0 ? 0 : r > 16 ? 2 : 1);
+}
+
+template <int NT, int ACT, bool GROUPED>
+ql_status launch_gemv_cfg(GvArgs p, int tiles, cudaStream_t st) {
+  const int units = gemv_units(p.N), kb = p.K / 128;
+  // enough CTAs for two on every SM, as far as K gives each warp a block
+  const int64_t ctas = static_cast<int64_t>(units) * tiles;
+  int S = static_cast<int>(std::min<int64_t>(kGvMaxCluster, std::max<int64_t>(1, 2 * num_sms() / ctas)));
+  S = std::min(S, (kb + 1) / 2);
+  if (S < 1) S = 1;
+  const int per_cta = (kb + S - 1) / S;
+  const int warps = std::min(kGvMaxWarps, per_cta);
+  p.cluster = S;
+  const int ring = warps * (kGvDepth * kGvStage + NT * 2048 + NT * 32);
+  const int red = (warps + 1) * 8 * NT * (kGvRows + 1) * 4;
+  const int smem = std::max(ring, red);
+  auto kern = k_gemv<NT, ACT, GROUPED>;
+  if (!set_smem_attr(reinterpret_cast<const void*>(kern), smem)) return QL_ERR_CUDA;
+  if (launch_pdl(kern, dim3(static_cast<unsigned>(units) * S, tiles), dim3(32 * warps), smem, st, S, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QL_ERR_CUDA;
+  }
+  return QL_OK;
+}
+
+}  // namespace
+
+ql_status launch_gemv(int act, const void* a, const float* a_scales, int64_t M, const ql_weights* w, void* Y,
+                      cudaStream_t st) {
+  if (M == 0) return QL_OK;
+  GvArgs p{};
+  p.a = static_cast<const uint8_t*>(a);
+  p.a_scales = a_scales;
+  p.codes = static_cast<const uint8_t*>(w->codes);
+  p.sf = static_cast<const uint8_t*>(w->sf);
+  p.gscale = w->gscale;
+  p.y = static_cast<__nv_bfloat16*>(Y);
+  p.rows_a = p.rows_y = M;
+  p.M = static_cast<int32_t>(M);
+  p.N = w->N;
+  p.K = w->K;
+  p.hadamard = w->hadamard;
+  p.alpha_mul = w->hadamard ? (1.0f / 128.0f) : 1.0f;
+  if (M <= 8)
+    return act == 0 ? launch_gemv_cfg<1, kGvBf16, false>(p, 1, st)
+           : act == 1 ? launch_gemv_cfg<1, kGvF16, false>(p, 1, st)
+                      : launch_gemv_cfg<1, kGvI8, false>(p, 1, st);
+  return act == 0 ? launch_gemv_cfg<2, kGvBf16, false>(p, 1, st)
+         : act == 1 ? launch_gemv_cfg<2, kGvF16, false>(p, 1, st)
+                    : launch_gemv_cfg<2, kGvI8, false>(p, 1, st);
+}
+
+}  // namespace ql

@@ -73,6 +73,9 @@ ql_status launch_tdc_refresh(const void* in, const void* out, int64_t numel, voi
 ql_status launch_tdc_skip(const void* in, int64_t numel, const void* slot0, const void* slot1,
                           ql_tdc_state* st, const ql_tdc_params& prm, void* out, int* status, cudaStream_t s);
 
+// 1 to 16 rows on NVFP4 weights; act: 0 bf16 rows, 1 f16 codes, 2 int8 codes.
+ql_status launch_gemv(int act, const void* a, const float* a_scales, int64_t M, const ql_weights* w, void* Y,
+                      cudaStream_t st);
 ql_status launch_gemm_w4a4(const void* a_codes, const uint8_t* a_sf, const float* g_a, int64_t M,
                            const ql_weights* w, void* Y, cudaStream_t st, int* status, Gate gate = {});
 // a_f16 = 1: activations are f16 [M, K] holding the INT8 codes (needs

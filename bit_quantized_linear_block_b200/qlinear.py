@@ -96,6 +96,7 @@ def _load() -> C.CDLL:
                                            vp, vp, vp, sz, vp]),
         "qlinear_norm_quantize": (C.c_int, [vp, vp, vp, i64, i32, f32, i32, i32, vp, vp, vp, vp, vp]),
         "qlinear_gemm": (C.c_int, [i32, vp, vp, vp, i64, C.POINTER(Weights), vp, vp]),
+        "qlinear_gemv": (C.c_int, [i32, vp, vp, i64, C.POINTER(Weights), vp, vp]),
         "qlinear_forward_ws_bytes": (sz, [i64, C.POINTER(Weights), i32]),
         "qlinear_forward": (C.c_int, [vp, i64, C.POINTER(Weights), i32, vp, vp, sz, vp]),
         "qlinear_forward_routed_ws_bytes": (sz, [i64, C.POINTER(Weights)]),
@@ -527,6 +528,37 @@ def qlinear_gemm(act_fmt: int, q: dict, M: int, w: PackedWeights, Y: torch.Tenso
         Y = _output(Y, M, w.N, dev)
         _check("qlinear_gemm", lib.qlinear_gemm(act_fmt, _ptr(codes), _ptr(q.get("sf_mma")), _ptr(q.get("scales")),
                                                 M, C.byref(w.desc), _ptr(Y), st))
+    return Y
+
+
+_GEMV_DTYPES = {QL_ROUTE_INT8: torch.int8, QL_ROUTE_INT6: torch.int8, QL_ACT_INT8_F16: torch.float16,
+                QL_ACT_INT6_F16: torch.float16, QL_ROUTE_BF16: torch.bfloat16}
+GEMV_MAX_ROWS = 16
+
+
+def qlinear_gemv(act_fmt: int, q: dict, M: int, w: PackedWeights, Y: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """qlinear_gemm for up to 16 rows (decoding), bound by reading the packed
+    NVFP4 weights once.  `q`: qlinear_quantize_act's or qlinear_norm_quantize's
+    dict for the per-token INT8 / INT6 formats; for QL_ROUTE_BF16
+    {"codes": the unquantized bf16 input}, rotated here when the weights are,
+    against the packed weights."""
+    _weights(w)
+    M = int(M)
+    if not 0 <= M <= GEMV_MAX_ROWS:
+        raise ValueError(f"M must be 0 to {GEMV_MAX_ROWS}, got {M}")
+    dtype = _GEMV_DTYPES.get(act_fmt)
+    if dtype is None:
+        raise ValueError(f"activation format {act_fmt} has no form for few rows")
+    codes = _tensor(q["codes"], "q['codes']", dtype, w.buf.device, M * w.K * dtype.itemsize)
+    dev = codes.device
+    scales = None
+    if act_fmt != QL_ROUTE_BF16:
+        scales = _tensor(q["scales"], "q['scales']", torch.float32, dev, 4 * M)
+    st = _stream(stream, dev)
+    with _call_on(dev, stream, codes, scales, w.buf):
+        Y = _output(Y, M, w.N, dev)
+        _check("qlinear_gemv", lib.qlinear_gemv(act_fmt, _ptr(codes), _ptr(scales), M, C.byref(w.desc), _ptr(Y), st))
     return Y
 
 

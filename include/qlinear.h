@@ -341,6 +341,25 @@ QL_API ql_status qlinear_gemm(int32_t act_fmt, const void* a_codes, const void* 
                        const float* a_scales, int64_t M, const ql_weights* w,
                        void* Y_bf16, void* stream);
 
+/* ---- few rows ---------------------------------------------------------------
+   The layer for M = 0 .. 16 rows (single decoded tokens and small batches) on
+   QL_W_NVFP4 weights, bound by reading the packed weights once; one launch, no
+   workspace.  More rows: QL_ERR_UNSUPPORTED_SHAPE (qlinear_gemm takes them).
+   QL_ROUTE_INT8, QL_ACT_INT8_F16, QL_ROUTE_INT6, QL_ACT_INT6_F16:
+                       qlinear_gemm's product on the same operands (exact
+                       products, fp32 sums in another order);
+   QL_ROUTE_BF16:      a = the unquantized bf16 input [M, K], a_scales unused;
+                       Y = bf16(g_w sum_k h[m,k] w[n,k]), h = H x and g_w / 128
+                       when the weights are rotated.  (qlinear_gemm's
+                       QL_ROUTE_BF16 multiplies the kept bf16 weights; this
+                       multiplies the packed ones.)  Each row's 128-element
+                       block of h is rounded to f16 after a power-of-two
+                       scaling: 2^-12 of a value that is not below 2^-29 of
+                       its block's largest.
+   Y must not overlap a.  A row with non-finite values affects no other row. */
+QL_API ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_scales, int64_t M,
+                              const ql_weights* w, void* Y_bf16, void* stream);
+
 /* ---- forward: quantize + GEMM ----------------------------------------------
    route: QL_ROUTE_NVFP4, QL_ROUTE_INT8 or QL_ROUTE_INT6 for NVFP4 weights
    (the activation rotation follows w->hadamard); for Q-ARVD weights

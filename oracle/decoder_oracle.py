@@ -41,3 +41,17 @@ def norm_quantize(x_bits, res_bits, gamma_bits, eps: float, hadamard: bool, qmax
     h, y = rms_norm(x_bits, res_bits, gamma_bits, eps)
     q, s = O.int8_per_token(O.block_hadamard(y) if hadamard else y, qmax)
     return h, y, q, s
+
+
+def nvfp4_product(a: np.ndarray, wq: dict, hadamard: bool, row_scale=None) -> np.ndarray:
+    """fp64 Y = alpha a W^T on oracle.qlinear_oracle's packed NVFP4 weights:
+    alpha = g_w (/128 for rotated weights) times the row's scale.  a: integer
+    codes (with row_scale), or unquantized rows (rotated here, in fp64, for
+    rotated weights)."""
+    a = np.asarray(a, dtype=np.float64)
+    if row_scale is None and hadamard:
+        a = (a.reshape(-1, O.HADAMARD_N) @ O.sylvester_hadamard(O.HADAMARD_N).astype(np.float64)).reshape(a.shape)
+    y = a @ O.nvfp4_dequantize(wq["packed"], wq["sb"]).T * np.float64(wq["g"])
+    if hadamard:
+        y = y / O.HADAMARD_N
+    return y if row_scale is None else y * np.asarray(row_scale, dtype=np.float64)[:, None]

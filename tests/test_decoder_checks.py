@@ -51,3 +51,40 @@ def test_norm_quantize_binding_checks(ql):
         ql.qlinear_norm_quantize(x.float(), g)
     with pytest.raises(TypeError, match="Tensor"):
         ql.qlinear_norm_quantize(None, g)
+
+
+def test_gemv_c_checks(ql):
+    a, sc, y = FAKE[:3]
+    w = ql.Weights(fmt=ql.QL_W_NVFP4, N=1920, K=1920, hadamard=1, codes=FAKE[3], sf=FAKE[4], gscale=FAKE[5])
+
+    def f(fmt=ql.QL_ROUTE_INT8, a=a, sc=sc, m=3, w=w, y=y):
+        return ql.lib.qlinear_gemv(fmt, a, sc, m, None if w is None else C.byref(w), y, None)
+
+    assert f(m=-1) == INVALID and f(m=17) == SHAPE and f(w=None) == INVALID
+    for fmt in (ql.QL_ROUTE_NVFP4, ql.QL_ACT_INT8_TENSOR, ql.QL_ACT_NVFP4_DECOMP, 99):
+        assert f(fmt=fmt) == INVALID
+    assert f(a=None) == INVALID and f(y=None) == INVALID and f(sc=None) == INVALID
+    assert f(a=a + 8) == ALIGN and f(y=y + 2) == ALIGN and f(sc=sc + 1) == ALIGN
+    for change, want in ((dict(K=100), SHAPE), (dict(N=20), SHAPE), (dict(fmt=ql.QL_W_NVFP4_DECOMP), INVALID),
+                         (dict(sf=None), INVALID), (dict(codes=None), INVALID)):
+        fields = dict(fmt=ql.QL_W_NVFP4, N=1920, K=1920, hadamard=1, codes=FAKE[3], sf=FAKE[4], gscale=FAKE[5])
+        assert f(w=ql.Weights(**{**fields, **change})) == want
+    q = ql.Weights(fmt=ql.QL_W_QARVD_INT4, N=256, K=256, Kp=288, codes=FAKE[3], gather=FAKE[4], kinfo=FAKE[4],
+                   s_norm=FAKE[4], s_out=FAKE[4])
+    assert f(w=q) == INVALID
+
+
+def test_gemv_binding_checks(ql):
+    with pytest.raises(TypeError, match="PackedWeights"):
+        ql.qlinear_gemv(ql.QL_ROUTE_INT8, {}, 1, object())
+    w = ql.PackedWeights(ql.Weights(), torch.zeros(256, dtype=torch.uint8), 16, 128, ql.QL_W_NVFP4)
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    for m in (-1, 17):
+        with pytest.raises(ValueError, match="0 to 16"):
+            ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x), m, w)
+    with pytest.raises(ValueError, match="format"):
+        ql.qlinear_gemv(ql.QL_ROUTE_NVFP4, dict(codes=x), 1, w)
+    with pytest.raises(TypeError, match="int8"):
+        ql.qlinear_gemv(ql.QL_ROUTE_INT8, dict(codes=x), 1, w)
+    with pytest.raises(ValueError, match="CUDA"):
+        ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x), 1, w)
