@@ -655,6 +655,75 @@ ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_scales, in
                      static_cast<cudaStream_t>(stream));
 }
 
+// ---------------------------------------------------------------- experts
+namespace {
+ql_status check_experts_shape(int64_t E, int64_t N, int64_t K) {
+  QL_TRY(check_k(K));
+  if (N <= 0 || N % 16 != 0 || N > (1 << 24)) return QL_ERR_UNSUPPORTED_SHAPE;
+  if (E <= 0 || E > 1024 || E * N >= (int64_t(1) << 31)) return QL_ERR_UNSUPPORTED_SHAPE;
+  return check_mk(N, K);
+}
+}  // namespace
+
+size_t qlinear_experts_bytes(int32_t E, int32_t N, int32_t K) {
+  if (check_experts_shape(E, N, K) != QL_OK) return 0;
+  const size_t e = E;
+  return align256(e * N * K / 2) + align256(e * qlinear_sf_bytes(N, K)) + align256(4 * e);
+}
+
+size_t qlinear_prepare_experts_ws_bytes(int32_t E, int32_t N, int32_t K) {
+  return check_experts_shape(E, N, K) == QL_OK ? kAmaxWsBytes + 256 : 0;
+}
+
+ql_status qlinear_prepare_experts(const void* W, int32_t E, int32_t N, int32_t K, int32_t hadamard, void* wbuf,
+                                  size_t wbuf_bytes, ql_experts* out, void* ws, size_t ws_bytes, void* stream) {
+  if (W == nullptr || wbuf == nullptr || out == nullptr || ws == nullptr) return QL_ERR_INVALID_ARG;
+  QL_TRY(check_experts_shape(E, N, K));
+  if (!aligned(W, 16) || !aligned(wbuf, 256) || !aligned(ws, 256)) return QL_ERR_ALIGNMENT;
+  if (wbuf_bytes < qlinear_experts_bytes(E, N, K) || ws_bytes < qlinear_prepare_experts_ws_bytes(E, N, K))
+    return QL_ERR_WORKSPACE;
+  QL_TRY(device_ready());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t codes = static_cast<size_t>(N) * K / 2, sf = qlinear_sf_bytes(N, K);
+  ql_experts w{};
+  w.E = E;
+  w.N = N;
+  w.K = K;
+  w.hadamard = hadamard ? 1 : 0;
+  Carver c{static_cast<uint8_t*>(wbuf)};
+  w.codes = c.take<uint8_t>(E * codes);
+  w.sf = c.take<uint8_t>(E * sf);
+  w.gscale = c.take<float>(4 * static_cast<size_t>(E));
+  float* amax = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAmaxWsBytes);
+  for (int32_t e = 0; e < E; ++e) {
+    const uint8_t* x = static_cast<const uint8_t*>(W) + e * codes * 4;
+    QL_TRY(launch_amax(x, N, K, w.hadamard, amax, ws, st));
+    QL_TRY(launch_quant_nvfp4(x, N, K, w.hadamard, amax, static_cast<uint8_t*>(w.codes) + e * codes,
+                              static_cast<uint8_t*>(w.sf) + e * sf, nullptr, w.gscale + e, st));
+  }
+  *out = w;
+  return QL_OK;
+}
+
+ql_status qlinear_grouped_gemm(int32_t act_fmt, const void* a_codes, const float* a_scales, int64_t rows_a,
+                               const int32_t* row_index, const int32_t* offsets, int64_t T, const ql_experts* w,
+                               void* Y, void* stream) {
+  QL_TRY(check_m(T));
+  QL_TRY(check_m(rows_a));
+  if (w == nullptr || w->codes == nullptr || w->sf == nullptr || w->gscale == nullptr) return QL_ERR_INVALID_ARG;
+  QL_TRY(check_experts_shape(w->E, w->N, w->K));
+  QL_TRY(check_mn(T, w->N));
+  if (int_base_fmt(act_fmt) != QL_ACT_INT8_F16) return QL_ERR_INVALID_ARG;
+  if (T > 0 && (a_codes == nullptr || a_scales == nullptr || offsets == nullptr || Y == nullptr || rows_a == 0))
+    return QL_ERR_INVALID_ARG;
+  if (!aligned(a_codes, 16) || !aligned(Y, 16) || !aligned(a_scales, 4) || !aligned(row_index, 4) ||
+      !aligned(offsets, 4))
+    return QL_ERR_ALIGNMENT;
+  QL_TRY(device_ready());
+  if (T == 0) return QL_OK;
+  return launch_grouped_few(a_codes, a_scales, rows_a, row_index, offsets, T, w, Y, static_cast<cudaStream_t>(stream));
+}
+
 // ---------------------------------------------------------------- forward
 size_t qlinear_forward_ws_bytes(int64_t M, const ql_weights* w, int32_t route) {
   if (M < 0 || check_w(w) != QL_OK) return 0;

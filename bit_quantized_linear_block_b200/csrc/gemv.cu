@@ -61,7 +61,7 @@ struct GvArgs {
   int64_t rows_a, rows_y;
   size_t expert_codes, expert_sf;
   int32_t M, N, K, E;
-  int32_t hadamard, cluster;
+  int32_t hadamard, cluster, units;
   float alpha_mul;
 };
 
@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
   const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
   const int S = p.cluster;
-  const int unit = blockIdx.x / S, rank = blockIdx.x - unit * S;
+  const int block = blockIdx.x / S, rank = blockIdx.x - block * S;
+  const int unit = GROUPED ? block % p.units : block;
   pdl_wait();
 
   int M = p.M;
@@ -219,8 +220,8 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
   const uint8_t* sf = p.sf;
   const float* gscale = p.gscale;
   if constexpr (GROUPED) {
-    // blockIdx.y counts the row tiles of all experts in order
-    int tile = blockIdx.y, e0 = 0;
+    // block / units counts the row tiles of all experts in order
+    int tile = block / p.units, e0 = 0;
     bool found = false;
     for (; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
@@ -471,23 +472,26 @@ int gemv_units(int32_t N) {
   return 2 * (N / 128) + (r == 0 ? 0 : r > 16 ? 2 : 1);
 }
 
+// tiles: row tiles (grouped: the most that the experts' rows can make).
 template <int NT, int ACT, bool GROUPED>
-ql_status launch_gemv_cfg(GvArgs p, int tiles, cudaStream_t st) {
+ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   const int units = gemv_units(p.N), kb = p.K / 128;
   // enough CTAs for two on every SM, as far as K gives each warp a block
-  const int64_t ctas = static_cast<int64_t>(units) * tiles;
+  const int64_t ctas = units * tiles;
   int S = static_cast<int>(std::min<int64_t>(kGvMaxCluster, std::max<int64_t>(1, 2 * num_sms() / ctas)));
   S = std::min(S, (kb + 1) / 2);
   if (S < 1) S = 1;
   const int per_cta = (kb + S - 1) / S;
   const int warps = std::min(kGvMaxWarps, per_cta);
+  if (ctas * S > 0x7FFFFFFF) return QL_ERR_UNSUPPORTED_SHAPE;
   p.cluster = S;
+  p.units = units;
   const int ring = warps * (kGvDepth * kGvStage + NT * 2048 + NT * 32);
   const int red = (warps + 1) * 8 * NT * (kGvRows + 1) * 4;
   const int smem = std::max(ring, red);
   auto kern = k_gemv<NT, ACT, GROUPED>;
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), smem)) return QL_ERR_CUDA;
-  if (launch_pdl(kern, dim3(static_cast<unsigned>(units) * S, tiles), dim3(32 * warps), smem, st, S, p) != cudaSuccess) {
+  if (launch_pdl(kern, dim3(static_cast<unsigned>(ctas * S)), dim3(32 * warps), smem, st, S, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return QL_ERR_CUDA;
   }
@@ -519,6 +523,32 @@ ql_status launch_gemv(int act, const void* a, const float* a_scales, int64_t M, 
   return act == 0 ? launch_gemv_cfg<2, kGvBf16, false>(p, 1, st)
          : act == 1 ? launch_gemv_cfg<2, kGvF16, false>(p, 1, st)
                     : launch_gemv_cfg<2, kGvI8, false>(p, 1, st);
+}
+
+ql_status launch_grouped_few(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
+                             const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st) {
+  GvArgs p{};
+  p.a = static_cast<const uint8_t*>(a);
+  p.a_scales = a_scales;
+  p.codes = static_cast<const uint8_t*>(w->codes);
+  p.sf = static_cast<const uint8_t*>(w->sf);
+  p.gscale = w->gscale;
+  p.y = static_cast<__nv_bfloat16*>(Y);
+  p.offsets = offsets;
+  p.rows = rows;
+  p.rows_a = rows_a;
+  p.rows_y = T;
+  p.expert_codes = static_cast<size_t>(w->N) * w->K / 2;
+  p.expert_sf = qlinear_sf_bytes(w->N, w->K);
+  p.N = w->N;
+  p.K = w->K;
+  p.E = w->E;
+  p.alpha_mul = w->hadamard ? (1.0f / 128.0f) : 1.0f;
+  auto tiles = [&](int64_t per) {   // sum of ceil(rows / per) over the experts, at most
+    const int64_t e = std::min<int64_t>(w->E, T);
+    return e + (T - e) / per;
+  };
+  return T <= 8 ? launch_gemv_cfg<1, kGvF16, true>(p, tiles(8), st) : launch_gemv_cfg<2, kGvF16, true>(p, tiles(16), st);
 }
 
 }  // namespace ql

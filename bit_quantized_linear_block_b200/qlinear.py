@@ -51,6 +51,11 @@ class Weights(C.Structure):
                 ("norms", C.c_void_p), ("w16", C.c_void_p), ("w8", C.c_void_p), ("wbf16", C.c_void_p)]
 
 
+class Experts(C.Structure):
+    _fields_ = [("E", C.c_int32), ("N", C.c_int32), ("K", C.c_int32), ("hadamard", C.c_int32),
+                ("codes", C.c_void_p), ("sf", C.c_void_p), ("gscale", C.c_void_p)]
+
+
 class TdcState(C.Structure):
     _fields_ = [("gamma", C.c_double), ("eps", C.c_double), ("acc", C.c_double), ("rho", C.c_double),
                 ("n_delta", C.c_int32), ("cur", C.c_int32), ("skips", C.c_int32), ("last_skipped", C.c_int32),
@@ -97,6 +102,10 @@ def _load() -> C.CDLL:
         "qlinear_norm_quantize": (C.c_int, [vp, vp, vp, i64, i32, f32, i32, i32, vp, vp, vp, vp, vp]),
         "qlinear_gemm": (C.c_int, [i32, vp, vp, vp, i64, C.POINTER(Weights), vp, vp]),
         "qlinear_gemv": (C.c_int, [i32, vp, vp, i64, C.POINTER(Weights), vp, vp]),
+        "qlinear_experts_bytes": (sz, [i32, i32, i32]),
+        "qlinear_prepare_experts_ws_bytes": (sz, [i32, i32, i32]),
+        "qlinear_prepare_experts": (C.c_int, [vp, i32, i32, i32, i32, vp, sz, C.POINTER(Experts), vp, sz, vp]),
+        "qlinear_grouped_gemm": (C.c_int, [i32, vp, vp, i64, vp, vp, i64, C.POINTER(Experts), vp, vp]),
         "qlinear_forward_ws_bytes": (sz, [i64, C.POINTER(Weights), i32]),
         "qlinear_forward": (C.c_int, [vp, i64, C.POINTER(Weights), i32, vp, vp, sz, vp]),
         "qlinear_forward_routed_ws_bytes": (sz, [i64, C.POINTER(Weights)]),
@@ -261,6 +270,54 @@ class PackedWeights:
                 raise ValueError(f"offset of {f} lies outside the weight buffer")
             setattr(desc, f, None if off is None else buf.data_ptr() + off)
         return cls(desc, buf, desc.N, desc.K, desc.fmt)
+
+
+@dataclass
+class PackedExperts:
+    """Packed NVFP4 weights of E experts of one shape: the C descriptor plus
+    the device buffer it points into."""
+    desc: Experts
+    buf: torch.Tensor
+    E: int
+    N: int
+    K: int
+
+    def expert(self, e: int) -> PackedWeights:
+        """Expert e's weights for the single-layer calls (a view of this buffer)."""
+        if not 0 <= e < self.E:
+            raise IndexError(f"expert {e} of {self.E}")
+        d = self.desc
+        desc = Weights(fmt=QL_W_NVFP4, N=self.N, K=self.K, hadamard=d.hadamard,
+                       codes=d.codes + e * (self.N * self.K // 2), sf=d.sf + e * lib.qlinear_sf_bytes(self.N, self.K),
+                       gscale=d.gscale + 4 * e)
+        return PackedWeights(desc, self.buf, self.N, self.K, QL_W_NVFP4)
+
+    def state_dict(self) -> dict:
+        """Host copy for a checkpoint, as PackedWeights.state_dict."""
+        base = self.buf.data_ptr()
+        return {"abi": lib.qlinear_abi_version(),
+                "sizes": {f: int(getattr(self.desc, f)) for f in ("E", "N", "K", "hadamard")},
+                "offsets": {f: getattr(self.desc, f) - base for f in ("codes", "sf", "gscale")},
+                "buf": self.buf.detach().to("cpu", copy=True)}
+
+    @classmethod
+    def from_state_dict(cls, sd: dict, device) -> "PackedExperts":
+        """Packed experts on `device` from state_dict()'s output (same ABI version)."""
+        if sd.get("abi") != lib.qlinear_abi_version():
+            raise ValueError(f"packed experts of ABI {sd.get('abi')}, this library is ABI {lib.qlinear_abi_version()}")
+        host, size = sd["buf"], {f: int(v) for f, v in sd["sizes"].items()}
+        if not isinstance(host, torch.Tensor) or host.dtype != torch.uint8 or host.dim() != 1:
+            raise TypeError("state_dict['buf'] must be a 1-D uint8 tensor")
+        E, N, K = size["E"], size["N"], size["K"]
+        need = {"codes": E * N * K // 2, "sf": E * lib.qlinear_sf_bytes(N, K), "gscale": 4 * E}
+        for f, n in need.items():
+            off = sd["offsets"][f]
+            if off < 0 or off % 256 != 0 or off + n > host.numel():
+                raise ValueError(f"{f} lies outside the weight buffer")
+        buf = torch.empty(host.numel(), dtype=torch.uint8, device=device)
+        buf.copy_(host)
+        desc = Experts(**size, **{f: buf.data_ptr() + sd["offsets"][f] for f in need})
+        return cls(desc, buf, E, N, K)
 
 
 # ----------------------------------------------------------------------------
@@ -559,6 +616,66 @@ def qlinear_gemv(act_fmt: int, q: dict, M: int, w: PackedWeights, Y: torch.Tenso
     with _call_on(dev, stream, codes, scales, w.buf):
         Y = _output(Y, M, w.N, dev)
         _check("qlinear_gemv", lib.qlinear_gemv(act_fmt, _ptr(codes), _ptr(scales), M, C.byref(w.desc), _ptr(Y), st))
+    return Y
+
+
+def qlinear_prepare_experts(W: torch.Tensor, hadamard: bool = True, stream=None) -> PackedExperts:
+    """NVFP4 weights of E experts from bf16 W [E, N, K]; expert e's are those
+    of qlinear_prepare_weights(W[e])."""
+    _tensor(W, "W", torch.bfloat16, dim=3)
+    dev = W.device
+    E, N, K = W.shape
+    wbytes = lib.qlinear_experts_bytes(E, N, K)
+    if wbytes == 0:
+        raise QLinearError("qlinear_experts_bytes", 2)
+    st = _stream(stream, dev)
+    with _call_on(dev, stream, W):
+        buf = _bytes(wbytes, dev)
+        ws = _bytes(lib.qlinear_prepare_experts_ws_bytes(E, N, K), dev)
+        desc = Experts()
+        _check("qlinear_prepare_experts",
+               lib.qlinear_prepare_experts(_ptr(W), E, N, K, int(bool(hadamard)), _ptr(buf), buf.numel(), C.byref(desc),
+                                           _ptr(ws), ws.numel(), st))
+    return PackedExperts(desc, buf, E, N, K)
+
+
+def qlinear_grouped_gemm(act_fmt: int, q: dict, offsets: torch.Tensor, w: PackedExperts,
+                         rows: torch.Tensor | None = None, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The layer grouped by expert: row r of segment [offsets[e],
+    offsets[e+1]) of Y is row `rows[r]` (r without `rows`) of the quantized
+    activations times expert e's weights.  `q`: the codes and scales of
+    QL_ACT_INT8_F16 or QL_ACT_INT6_F16; `offsets`: int32 [E + 1]; `rows`:
+    int32, one per row of Y (a token may appear in many rows).  Y has
+    Y.shape[0], rows.numel() or the codes' row count; its rows outside every
+    segment are left as they are (unset in a Y made here).  Offsets and rows
+    stay on the device: no synchronization."""
+    if not isinstance(w, PackedExperts):
+        raise TypeError(f"w must be PackedExperts (from qlinear_prepare_experts), got {type(w).__name__}")
+    if act_fmt not in (QL_ACT_INT8_F16, QL_ACT_INT6_F16):
+        raise ValueError(f"activation format {act_fmt} has no grouped form")
+    dev = w.buf.device
+    codes = _tensor(q["codes"], "q['codes']", torch.float16, dev, dim=2)
+    n_src = codes.shape[0]
+    if codes.shape[1] != w.K:
+        raise ValueError(f"q['codes'] has {codes.shape[1]} columns, the weights take K = {w.K}")
+    scales = _tensor(q["scales"], "q['scales']", torch.float32, dev, 4 * n_src)
+    _tensor(offsets, "offsets", torch.int32, dev, dim=1)
+    if offsets.numel() != w.E + 1:
+        raise ValueError(f"offsets has {offsets.numel()} elements, {w.E} experts need {w.E + 1}")
+    T = n_src
+    if rows is not None:
+        T = _tensor(rows, "rows", torch.int32, dev, dim=1).numel()
+    if Y is not None:
+        _tensor(Y, "Y", torch.bfloat16, dev, dim=2)
+        if Y.shape[1] != w.N or Y.shape[0] != T:
+            raise ValueError(f"Y is {tuple(Y.shape)}, the call writes {(T, w.N)}")
+    st = _stream(stream, dev)
+    with _call_on(dev, stream, codes, scales, offsets, rows, w.buf):
+        if Y is None:
+            Y = torch.empty((T, w.N), dtype=torch.bfloat16, device=dev)
+        _check("qlinear_grouped_gemm",
+               lib.qlinear_grouped_gemm(act_fmt, _ptr(codes), _ptr(scales), n_src, _ptr(rows), _ptr(offsets), T,
+                                        C.byref(w.desc), _ptr(Y), st))
     return Y
 
 

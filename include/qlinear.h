@@ -164,6 +164,17 @@ typedef struct {
                             given (not rotated); NULL otherwise                 */
 } ql_weights;
 
+/* Packed weights of E experts of one shape.  Filled by
+   qlinear_prepare_experts(); the pointers point into the caller's weight
+   buffer.  Treat as read-only. */
+typedef struct {
+  int32_t E, N, K, hadamard;
+  void* codes;           /* NVFP4 codes [E, N, K/2]                             */
+  void* sf;              /* block scales, MMA layout, qlinear_sf_bytes(N, K)
+                            bytes per expert                                    */
+  float* gscale;         /* fp32 tensor scale of each expert [E]                */
+} ql_experts;
+
 /* ---- library ------------------------------------------------------------ */
 
 QL_API int qlinear_abi_version(void);
@@ -359,6 +370,37 @@ QL_API ql_status qlinear_gemm(int32_t act_fmt, const void* a_codes, const void* 
    Y must not overlap a.  A row with non-finite values affects no other row. */
 QL_API ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_scales, int64_t M,
                               const ql_weights* w, void* Y_bf16, void* stream);
+
+/* ---- experts -----------------------------------------------------------------
+   The layer with tokens routed to experts: row segment e of the output is the
+   product of its rows with expert e's weights.
+   qlinear_prepare_experts: W is bf16 [E, N, K]; expert e's codes, scales and
+   tensor scale are what qlinear_prepare_weights gives for W[e] (QL_W_NVFP4).
+   E <= 1024, E * N < 2^31.  ws as for qlinear_prepare_weights.  Asynchronous.
+
+   qlinear_grouped_gemm: for every expert e and row r in
+   [offsets[e], offsets[e+1]):
+     src = row_index ? row_index[r] : r
+     Y[r, :] = bf16(s[src] g_e sum_k q[src, k] W_e[n, k])  (/128 if rotated)
+   act_fmt: QL_ACT_INT8_F16 or QL_ACT_INT6_F16 (the codes and scales of
+   qlinear_quantize_act or qlinear_norm_quantize): q f16 [rows_a, K], s fp32
+   [rows_a].  offsets: device int32 [E + 1], ascending; row_index: device
+   int32 [T] (a token may appear in many rows), or NULL; Y: bf16 [T, N].
+   Neither is read on the host, so the call does not synchronize and can be
+   captured; replays follow the values that they then hold.  Rows of Y outside
+   every segment are left as they are.  An offset outside [0, T] counts as the
+   nearer end and a descending pair as an empty segment (where that makes
+   segments overlap, rows inside segments are unspecified); a source row
+   outside [0, rows_a) gives a row of zeros.  Y must not overlap an operand.
+   4-byte aligned offsets and row_index; one launch, no workspace. */
+QL_API size_t qlinear_experts_bytes(int32_t E, int32_t N, int32_t K);
+QL_API size_t qlinear_prepare_experts_ws_bytes(int32_t E, int32_t N, int32_t K);
+QL_API ql_status qlinear_prepare_experts(const void* W_bf16, int32_t E, int32_t N, int32_t K, int32_t hadamard,
+                                         void* wbuf, size_t wbuf_bytes, ql_experts* out, void* ws,
+                                         size_t ws_bytes, void* stream);
+QL_API ql_status qlinear_grouped_gemm(int32_t act_fmt, const void* a_codes, const float* a_scales, int64_t rows_a,
+                                      const int32_t* row_index, const int32_t* offsets, int64_t T,
+                                      const ql_experts* w, void* Y_bf16, void* stream);
 
 /* ---- forward: quantize + GEMM ----------------------------------------------
    route: QL_ROUTE_NVFP4, QL_ROUTE_INT8 or QL_ROUTE_INT6 for NVFP4 weights

@@ -55,3 +55,19 @@ def nvfp4_product(a: np.ndarray, wq: dict, hadamard: bool, row_scale=None) -> np
     if hadamard:
         y = y / O.HADAMARD_N
     return y if row_scale is None else y * np.asarray(row_scale, dtype=np.float64)[:, None]
+
+
+def grouped_product(codes, scales, rows, offsets, experts, hadamard: bool, y: np.ndarray) -> np.ndarray:
+    """fp64 rows of Y by expert: Y[r] = codes[src] . experts[e] times the
+    scales, src = rows[r] (r without rows), for r in [offsets[e],
+    offsets[e+1]); a source row that does not exist gives zeros; rows outside
+    every segment keep `y`'s values."""
+    out = np.array(y, dtype=np.float64)
+    for e, wq in enumerate(experts):
+        for r in range(offsets[e], offsets[e + 1]):
+            src = r if rows is None else int(rows[r])
+            if 0 <= src < len(codes):
+                out[r] = nvfp4_product(codes[src:src + 1], wq, hadamard, scales[src:src + 1])[0]
+            else:
+                out[r] = 0.0
+    return out

@@ -88,3 +88,61 @@ def test_gemv_binding_checks(ql):
         ql.qlinear_gemv(ql.QL_ROUTE_INT8, dict(codes=x), 1, w)
     with pytest.raises(ValueError, match="CUDA"):
         ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x), 1, w)
+
+
+def test_experts_c_checks(ql):
+    L = ql.lib
+    assert L.qlinear_experts_bytes(4, 1920, 1920) >= 4 * (1920 * 960 + 1920 * 120)
+    for e, n, k in ((0, 64, 128), (1025, 64, 128), (4, 20, 128), (4, 64, 100), (1024, 1 << 21, 128)):
+        assert L.qlinear_experts_bytes(e, n, k) == 0 and L.qlinear_prepare_experts_ws_bytes(e, n, k) == 0
+    desc = ql.Experts()
+
+    def prep(w=FAKE[0], e=4, n=64, k=128, buf=FAKE[1], size=1 << 30, ws=FAKE[2], ws_size=1 << 30):
+        return L.qlinear_prepare_experts(w, e, n, k, 1, buf, size, C.byref(desc), ws, ws_size, None)
+
+    assert prep(w=None) == INVALID and prep(buf=None) == INVALID and prep(ws=None) == INVALID
+    assert prep(e=0) == SHAPE and prep(n=8) == SHAPE and prep(k=64) == SHAPE
+    assert prep(w=FAKE[0] + 8) == ALIGN and prep(buf=FAKE[1] + 16) == ALIGN
+    assert prep(size=64) == 6 and prep(ws_size=64) == 6
+
+    good = dict(E=4, N=64, K=128, hadamard=1, codes=FAKE[3], sf=FAKE[4], gscale=FAKE[5])
+
+    def f(fmt=ql.QL_ACT_INT8_F16, a=FAKE[0], sc=FAKE[1], n_a=8, rows=None, off=FAKE[2], t=8, w=good, y=FAKE[6]):
+        return L.qlinear_grouped_gemm(fmt, a, sc, n_a, rows, off, t, None if w is None else C.byref(ql.Experts(**w)), y,
+                                      None)
+
+    assert f(t=-1) == INVALID and f(n_a=-1) == INVALID and f(n_a=0) == INVALID and f(w=None) == INVALID
+    for name in ("a", "sc", "off", "y"):
+        assert f(**{name: None}) == INVALID
+    for name in ("codes", "sf", "gscale"):
+        assert f(w={**good, name: None}) == INVALID
+    for change in (dict(E=0), dict(E=2000), dict(N=24), dict(K=64)):
+        assert f(w={**good, **change}) == SHAPE
+    for fmt in (ql.QL_ROUTE_INT8, ql.QL_ROUTE_BF16, ql.QL_ROUTE_NVFP4, ql.QL_ACT_INT8_TENSOR, 99):
+        assert f(fmt=fmt) == INVALID
+    assert f(a=FAKE[0] + 2) == ALIGN and f(y=FAKE[6] + 2) == ALIGN
+    assert f(off=FAKE[2] + 2) == ALIGN and f(rows=FAKE[7] + 2) == ALIGN and f(sc=FAKE[1] + 2) == ALIGN
+
+
+def test_experts_binding_checks(ql):
+    with pytest.raises(ValueError, match="CUDA"):
+        ql.qlinear_prepare_experts(torch.zeros(2, 16, 128, dtype=torch.bfloat16))
+    with pytest.raises(TypeError, match="PackedExperts"):
+        ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, {}, None, object())
+    w = ql.PackedExperts(ql.Experts(E=2, N=16, K=128, codes=1 << 20, sf=1 << 20, gscale=1 << 20),
+                         torch.zeros(256, dtype=torch.uint8), 2, 16, 128)
+    with pytest.raises(ValueError, match="grouped"):
+        ql.qlinear_grouped_gemm(ql.QL_ROUTE_INT8, {}, None, w)
+    q = dict(codes=torch.zeros(4, 128, dtype=torch.float16), scales=torch.zeros(4))
+    with pytest.raises(ValueError, match="CUDA"):
+        ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, torch.zeros(3, dtype=torch.int32), w)
+    with pytest.raises(IndexError):
+        w.expert(2)
+    sd = dict(abi=ql.lib.qlinear_abi_version(), sizes=dict(E=2, N=16, K=128, hadamard=1),
+              offsets=dict(codes=0, sf=2048, gscale=4096 + 2048), buf=torch.zeros(8192, dtype=torch.uint8))
+    ok = ql.PackedExperts.from_state_dict(sd, "cpu")
+    assert (ok.E, ok.N, ok.K) == (2, 16, 128) and ok.desc.sf - ok.desc.codes == 2048
+    for change in (dict(abi=0), dict(offsets={**sd["offsets"], "gscale": 8192}),
+                   dict(offsets={**sd["offsets"], "sf": 100})):
+        with pytest.raises(ValueError):
+            ql.PackedExperts.from_state_dict({**sd, **change}, "cpu")
