@@ -721,7 +721,10 @@ ql_status qlinear_grouped_gemm(int32_t act_fmt, const void* a_codes, const float
     return QL_ERR_ALIGNMENT;
   QL_TRY(device_ready());
   if (T == 0) return QL_OK;
-  return launch_grouped_few(a_codes, a_scales, rows_a, row_index, offsets, T, w, Y, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T <= 16 || T <= 4 * static_cast<int64_t>(w->E))
+    return launch_grouped_few(a_codes, a_scales, rows_a, row_index, offsets, T, w, Y, st);
+  return launch_gemm_grouped(a_codes, a_scales, rows_a, row_index, offsets, T, w, Y, st, status_word());
 }
 
 // ---------------------------------------------------------------- forward

@@ -1,0 +1,468 @@
+// The quantized linear layer grouped by expert: ragged row segments of
+// f16-coded integer activations, each times its own expert's NVFP4 weights.
+//
+//   Y[r, n] = bf16(RN(RN(g_e alpha_mul) s[src]) * sum_k q[src, k] W_e[n, k]),
+//   r in [offsets[e], offsets[e+1]), src = rows[r] (or r)
+//
+// Bound: the tensor cores when experts have many rows (2 T N K flop), the
+// packed weights' bytes when they have few.  The weights are widened on chip:
+// E2M1 x E4M3 is exact in f16, and a tcgen05.mma takes its A operand from
+// tensor memory, so the kernel computes the transposed tile
+// D[n, m] = sum_k W[n, k] q[m, k] (128 weight rows on the TMEM lanes, up to
+// BMT rows of q as the MMA's N) and the widened weights never pass through
+// shared memory.
+//
+// Tiles.  The segments' lengths are on the device only, so every CTA builds
+// the tile table itself from the offsets: expert e with c rows makes
+// ceil(c / BMT) row tiles of equal height (rounded up to 16, the MMA's N
+// step), each times ceil(N / 128) weight tiles, weight tiles fastest (the
+// CTAs that run together share a row tile and sweep one expert's weights).
+// A tile costs what its rows need: the MMA's N, the loaded boxes and the
+// stored boxes follow its height.
+//
+// Persistent, one CTA per SM, warps by role:
+//   warp 0      TMA producer: the activation tile (64-row boxes, or
+//               four-row gathers through `rows`; 128-byte swizzle), the FP4
+//               weight tile and its scales, into an RS-deep ring of 64-deep
+//               K stages;
+//   warp 1      TMEM allocator and MMA issuer (kind::f16, A from tensor memory);
+//   4 XG warps  transform: group g widens the stages with it % XG == g, lane
+//               l of lane quarter q its weight row 32 q + l, into one of AS
+//               32-column slots of tensor memory;
+//   8 warps     epilogue: a TMEM lane quarter each, every other 32-row box:
+//               scale, bf16, and a TMA store of the 32 x 32 box through the
+//               warp's own staging buffer.  A box that reaches past its
+//               segment is stored row by row, so no row of another segment
+//               or behind the last one is written.
+// All waits are bounded; on a timeout a role records it, drains its own
+// copies or MMAs and leaves the loop, and the CTA frees its tensor memory.
+#include "ql_common.cuh"
+#include "gemm_common.cuh"
+#include "launchers.h"
+#include "segments.cuh"
+
+namespace ql {
+
+constexpr int kMaxExperts = 1024;
+
+struct GroupedArgs {
+  const int32_t* offsets;
+  const int32_t* rows;       // null: row r of Y is row r of the activations
+  const float* row_scale;    // [rows_a]
+  const float* g_w;          // [E]
+  const uint8_t* sf;
+  __nv_bfloat16* y;
+  size_t expert_sf;
+  int64_t rows_a, T;
+  int32_t E, N, K;
+  int32_t tiles_n, num_kst, k_atoms;
+  float alpha_mul;
+  long long wait_limit;
+  int* status;
+};
+
+template <int BMT, int RS, int XG>
+struct GroupedCfg {
+  static constexpr int BK = 64;
+  static constexpr int NACC = (2 * BMT + 4 * 32 <= 512) ? 2 : 1;
+  static constexpr int AS = (512 - NACC * BMT) / 32 < 8 ? (512 - NACC * BMT) / 32 : 8;   // A slots
+  static constexpr int B_BYTES = BMT * BK * 2;
+  static constexpr int W_BYTES = 128 * BK / 2;
+  static constexpr int SF_BYTES = 512;
+  static constexpr int OFF_B = 0;
+  static constexpr int OFF_W = OFF_B + RS * B_BYTES;
+  static constexpr int OFF_SF = OFF_W + RS * W_BYTES;
+  static constexpr int OFF_C = OFF_SF + RS * SF_BYTES;
+  static constexpr int OFF_TAB = OFF_C + 8 * 2 * kWarpBoxBytes;      // first tile, first row, rows of each expert
+  static constexpr int OFF_BAR = OFF_TAB + 3 * 4 * (kMaxExperts + 4);
+  static constexpr int NBAR = 2 * RS + 2 * AS + 2 * 2 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static constexpr int EPI0 = 4 + 4 * XG;
+  static constexpr int THREADS = (EPI0 + 8) * 32;
+  static_assert(XG >= 1 && XG <= 3, "transform warp groups");
+  static_assert(AS >= 2, "tensor memory budget");
+  static_assert(BMT % 64 == 0, "whole activation boxes");
+  static_assert(OFF_BAR % 8 == 0, "mbarrier alignment");
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// kind::f16: D = F32, A = B = F16, both K-major, M = 128, N = n (a multiple of 16)
+__device__ __forceinline__ uint32_t grouped_idesc(int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// Four rows of a 2-D tensor (one 128-byte piece each) to consecutive
+// 128-byte rows of shared memory.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int4 r) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
+      : "memory");
+}
+
+struct GroupedTile {
+  int e, nb;       // expert, weight tile
+  int row0, rows;  // rows [row0, row0 + rows) of Y
+  int n;           // rows rounded up to the MMA's step
+};
+
+// Walks the tile table in ascending tile order.
+struct TileCursor {
+  const int* first;   // first row tile of each expert, [E] the total
+  const int* lo;
+  const int* cnt;
+  int e;
+  __device__ __forceinline__ GroupedTile at(int t, int tiles_n, int bmt) {
+    const int tt = t / tiles_n;
+    while (first[e + 1] <= tt) ++e;
+    const int count = cnt[e], nt = first[e + 1] - first[e];
+    const int per = ((count + nt - 1) / nt + 15) & ~15;
+    const int start = (tt - first[e]) * per;
+    GroupedTile r;
+    r.e = e;
+    r.nb = t - tt * tiles_n;
+    r.row0 = lo[e] + start;
+    r.rows = min(per, count - start);
+    r.n = (r.rows + 15) & ~15;
+    return r;
+  }
+};
+
+// Lane 0 waits for one or two mbarriers, the warp shares the outcome.
+__device__ __forceinline__ bool warp_wait_pair(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, long long limit,
+                                               volatile int* abort_flag) {
+  int ok = 0;
+  if (lane_id() == 0)
+    ok = (*abort_flag == 0) && mbar_wait(a, pa, limit) && (b == nullptr || mbar_wait(b, pb, limit));
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+template <int BMT, int RS, int XG>
+__global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
+    k_gemm_grouped(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                   const __grid_constant__ CUtensorMap tm_y, const GroupedArgs p) {
+  using C = GroupedCfg<BMT, RS, XG>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_1024(smem_raw);
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* raw_empty = raw_full + RS;
+  uint64_t* xf_full = raw_empty + RS;
+  uint64_t* xf_empty = xf_full + C::AS;
+  uint64_t* tfull = xf_empty + C::AS;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* s_first = reinterpret_cast<int*>(smem + C::OFF_TAB);
+  int* s_lo = s_first + kMaxExperts + 4;
+  int* s_cnt = s_lo + kMaxExperts + 4;
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = lane_id();
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tm_x);
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_y);
+    for (int i = 0; i < RS; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 1);
+    }
+    for (int i = 0; i < C::AS; ++i) {
+      mbar_init(&xf_full[i], 4);
+      mbar_init(&xf_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 8);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  pdl_wait();
+  if (warp == 0) {   // the tile table
+    int total = 0;
+    int64_t carry = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + static_cast<int>(lane);
+      int64_t lo, hi;
+      warp_segments(p.offsets, p.E, p.T, e, carry, lo, hi);
+      const int cnt = static_cast<int>(hi - lo), tiles = (cnt + BMT - 1) / BMT;
+      const int end = warp_inclusive_sum(tiles);
+      if (e < p.E) {
+        s_first[e] = total + end - tiles;
+        s_lo[e] = static_cast<int>(lo);
+        s_cnt[e] = cnt;
+      }
+      total += __shfl_sync(0xffffffffu, end, 31);
+    }
+    if (lane == 0) s_first[p.E] = total;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t a_slots = tmem + C::NACC * BMT;
+  const int num_tiles = s_first[p.E] * p.tiles_n;
+  TileCursor cur{s_first, s_lo, s_cnt, 0};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    int it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+      const GroupedTile g = cur.at(t, p.tiles_n, BMT);
+      const int boxes = (g.n + 63) >> 6;
+      int4 src[2];   // gathers: source rows of four-row groups lane and lane + 32
+      if (p.rows != nullptr) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          int r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // rows past the tile's last repeat it; a row that does not exist
+            // reads row 0 and gets scale 0 in the epilogue
+            const int m = min(4 * (static_cast<int>(lane) + 32 * h) + i, g.rows - 1);
+            const int v = p.rows[static_cast<int64_t>(g.row0) + m];
+            r[i] = v >= 0 && v < p.rows_a ? v : 0;
+          }
+          src[h] = make_int4(r[0], r[1], r[2], r[3]);
+        }
+      }
+      const uint8_t* sf = p.sf + static_cast<size_t>(g.e) * p.expert_sf + static_cast<size_t>(g.nb) * p.k_atoms * 512;
+      const int wrow = g.e * p.N + g.nb * 128;
+      for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
+        const int s = it % RS;
+        if (!warp_wait_pair(&raw_empty[s], ((it / RS) & 1) ^ 1, nullptr, 0, p.wait_limit, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t* b = smem + C::OFF_B + s * C::B_BYTES;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&raw_full[s],
+                                (p.rows != nullptr ? g.n * 128 : boxes * 8192) + C::W_BYTES + C::SF_BYTES);
+          tma_load_2d(smem + C::OFF_W + s * C::W_BYTES, &tm_w, &raw_full[s], ks * (C::BK / 2), wrow);
+          bulk_load(smem + C::OFF_SF + s * C::SF_BYTES, sf + static_cast<size_t>(ks) * 512, C::SF_BYTES, &raw_full[s]);
+          if (p.rows == nullptr)
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(b + i * 8192, &tm_x, &raw_full[s], ks * C::BK, g.row0 + 64 * i);
+        }
+        if (p.rows != nullptr) {
+          __syncwarp();   // the byte count is set before any gather can complete
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int i = static_cast<int>(lane) + 32 * h;
+            if (4 * i < g.n) tma_gather4(b + i * 512, &tm_x, &raw_full[s], ks * C::BK, src[h]);
+          }
+        }
+      }
+    }
+    if (lane == 0) {
+      if (!ok) fail_timeout(p.status, abort_flag);
+      drain_loads(raw_full, it, RS, p.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (elect_one()) {
+      int it = 0, local = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++local) {
+        const uint32_t idesc = grouped_idesc(cur.at(t, p.tiles_n, BMT).n);
+        const int acc = local % C::NACC;
+        if (*abort_flag || !mbar_wait(&tempty[acc], ((local / C::NACC) & 1) ^ 1, p.wait_limit)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + acc * BMT;
+        for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
+          const int rs = it % RS, sl = it % C::AS;
+          if (*abort_flag || !mbar_wait(&raw_full[rs], (it / RS) & 1, p.wait_limit) ||
+              !mbar_wait(&xf_full[sl], (it / C::AS) & 1, p.wait_limit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t b_base = smem_u32(smem + C::OFF_B + rs * C::B_BYTES);
+#pragma unroll
+          for (int i = 0; i < C::BK / 16; ++i)
+            tc_mma_f16_ts(d_tmem, a_slots + 32 * sl + 8 * i, smem_desc(b_base + 32 * i, 0, 1024, kSwizzle128B), idesc,
+                          (ks > 0 || i > 0) ? 1u : 0u);
+          tc_commit(&raw_empty[rs]);
+          tc_commit(&xf_empty[sl]);
+        }
+        if (!ok) break;
+        tc_commit(&tfull[acc]);
+      }
+      if (!ok) fail_timeout(p.status, abort_flag);
+      drain_mma(drain, p.status);
+    }
+  } else if (warp >= 4 && warp < C::EPI0) {
+    // ------------------------------------------------------------ transform
+    const uint32_t q = static_cast<uint32_t>(warp & 3);
+    const uint32_t row = 32 * q + lane;
+    const int group = (warp - 4) >> 2;
+    int it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+      for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
+        if (it % XG != group) continue;
+        const int rs = it % RS, sl = it % C::AS;
+        if (!warp_wait_pair(&raw_full[rs], (it / RS) & 1, &xf_empty[sl], ((it / C::AS) & 1) ^ 1, p.wait_limit,
+                            abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // scale atom: byte (row % 32) * 16 + (row / 32) * 4 + k16 holds the block scale of K block k16
+        const uint32_t sb4 = *reinterpret_cast<const uint32_t*>(smem + C::OFF_SF + rs * C::SF_BYTES + lane * 16 + q * 4);
+        const uint4* wr = reinterpret_cast<const uint4*>(smem + C::OFF_W + rs * C::W_BYTES + row * 32);
+        const uint4 c0 = wr[0], c1 = wr[1];
+        const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        uint32_t v[32];
+#pragma unroll
+        for (int w8 = 0; w8 < 8; ++w8) {
+          const uint4 o = fp4x8_scaled_to_f16(cw[w8], (sb4 >> (8 * (w8 >> 1))) & 0xFFu);
+          v[4 * w8] = o.x;
+          v[4 * w8 + 1] = o.y;
+          v[4 * w8 + 2] = o.z;
+          v[4 * w8 + 3] = o.w;
+        }
+        tmem_st32(a_slots + ((32 * q) << 16) + 32 * sl, v);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&xf_full[sl]);
+      }
+    }
+    if (!ok && lane == 0) fail_timeout(p.status, abort_flag);
+  } else if (warp >= C::EPI0) {
+    // ------------------------------------------------------------ epilogue
+    const uint32_t q = static_cast<uint32_t>(warp & 3);
+    const int half = (warp - C::EPI0) >> 2;
+    uint8_t* stage = smem + C::OFF_C + (warp - C::EPI0) * 2 * kWarpBoxBytes;
+    int next = 0, local = 0;
+    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++local) {
+      const GroupedTile g = cur.at(t, p.tiles_n, BMT);
+      const int acc = local % C::NACC;
+      if (!warp_wait_uniform(&tfull[acc], (local / C::NACC) & 1, p.wait_limit, abort_flag, p.status)) break;
+      tc_fence_after();
+      const float alpha = __fmul_rn(ld_dep(p.g_w + g.e), p.alpha_mul);
+      const int n0 = g.nb * 128 + 32 * static_cast<int>(q);
+      const int boxes = n0 < p.N ? (g.rows + 31) >> 5 : 0;       // this warp's: half, half + 2, ...
+      for (int c = half; c < boxes; c += 2) {
+        uint32_t r[32];
+        tmem_ld32(tmem + ((32 * q) << 16) + acc * BMT + 32 * c, r);
+        const int m = 32 * c + static_cast<int>(lane);           // row of the tile
+        float a_l = 0.f;
+        if (m < g.rows) {
+          int64_t src = static_cast<int64_t>(g.row0) + m;
+          if (p.rows != nullptr) src = p.rows[src];
+          if (src >= 0 && src < p.rows_a) a_l = __fmul_rn(alpha, ld_dep(p.row_scale + src));
+        }
+        tmem_ld_wait();
+        if (c + 2 >= boxes) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc]);
+        }
+        if (32 * c + 32 <= g.rows) {
+          uint8_t* buf = stage + next * kWarpBoxBytes;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(buf) + lane;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            dst[32 * j] = __float2bfloat16_rn(__fmul_rn(__shfl_sync(0xffffffffu, a_l, j), __uint_as_float(r[j])));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_y, buf, n0, g.row0 + 32 * c);
+            bulk_commit();
+          }
+          next ^= 1;
+        } else {
+          const int n = n0 + static_cast<int>(lane);
+          __nv_bfloat16* dst = p.y + (static_cast<int64_t>(g.row0) + 32 * c) * p.N + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float v = __fmul_rn(__shfl_sync(0xffffffffu, a_l, j), __uint_as_float(r[j]));
+            if (32 * c + j < g.rows && n < p.N) dst[static_cast<int64_t>(j) * p.N] = __float2bfloat16_rn(v);
+          }
+        }
+      }
+      if (half >= boxes) {   // no box: nothing was read
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(&tempty[acc]);
+      }
+    }
+    epilogue_warp_finish();
+  }
+
+  pdl_release();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int BMT, int RS, int XG>
+static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
+                                    const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
+                                    int* status) {
+  using C = GroupedCfg<BMT, RS, XG>;
+  const int N = w->N, K = w->K;
+  CUtensorMap tx, tw, ty;
+  if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows_a, static_cast<int64_t>(K) * 2, C::BK,
+                    rows != nullptr ? 1 : 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, static_cast<int64_t>(w->E) * N, K / 2,
+                    C::BK / 2, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, T, static_cast<int64_t>(N) * 2, 32, 32,
+                    CU_TENSOR_MAP_SWIZZLE_NONE))
+    return QL_ERR_CUDA;
+  GroupedArgs p{};
+  GemmArgs limits{};
+  fill_gemm_args(limits, T, N, K, 128, status);
+  p.offsets = offsets;
+  p.rows = rows;
+  p.row_scale = a_scales;
+  p.g_w = w->gscale;
+  p.sf = static_cast<const uint8_t*>(w->sf);
+  p.y = static_cast<__nv_bfloat16*>(Y);
+  p.expert_sf = qlinear_sf_bytes(N, K);
+  p.rows_a = rows_a;
+  p.T = T;
+  p.E = w->E;
+  p.N = N;
+  p.K = K;
+  p.tiles_n = (N + 127) / 128;
+  p.num_kst = K / C::BK;
+  p.k_atoms = K / 64;
+  p.alpha_mul = w->hadamard ? (1.0f / 128.0f) : 1.0f;
+  p.wait_limit = limits.wait_limit;
+  p.status = status;
+  // the most tiles that the rows can make
+  const int64_t e = std::min<int64_t>(w->E, T);
+  const int64_t tiles = (e + (T - e) / BMT) * p.tiles_n;
+  if (tiles > 0x7FFFFFFF - num_sms()) return QL_ERR_UNSUPPORTED_SHAPE;
+  auto kern = k_gemm_grouped<BMT, RS, XG>;
+  if (!set_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return QL_ERR_CUDA;
+  const int grid = static_cast<int>(std::min<int64_t>(tiles, num_sms()));
+  if (launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, st, 1, tx, tw, ty, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QL_ERR_CUDA;
+  }
+  return QL_OK;
+}
+
+ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
+                              const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
+                              int* status) {
+  return launch_grouped_cfg<192, 6, 2>(a, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+}
+
+}  // namespace ql

@@ -35,6 +35,7 @@
 #include "ql_common.cuh"
 #include "gemm_common.cuh"
 #include "launchers.h"
+#include "segments.cuh"
 
 namespace ql {
 
@@ -223,21 +224,12 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
     // block / units counts the row tiles of all experts in order
     int tile = block / p.units, e0 = 0;
     bool found = false;
+    int64_t carry = 0;
     for (; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      int64_t lo = 0;
-      int cnt = 0;
-      if (e < p.E) {
-        lo = min(max(static_cast<int64_t>(p.offsets[e]), int64_t(0)), p.rows_y);
-        cnt = static_cast<int>(min(max(static_cast<int64_t>(p.offsets[e + 1]), lo), p.rows_y) - lo);
-      }
-      const int tiles = (cnt + kTokens - 1) / kTokens;
-      int end = tiles;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, end, o);
-        if (lane >= o) end += v;
-      }
+      int64_t lo, hi;
+      warp_segments(p.offsets, p.E, p.rows_y, e0 + lane, carry, lo, hi);
+      const int cnt = static_cast<int>(hi - lo), tiles = (cnt + kTokens - 1) / kTokens;
+      const int end = warp_inclusive_sum(tiles);
       const unsigned hit = __ballot_sync(0xffffffffu, tile < end);
       if (hit != 0) {
         const int src = __ffs(hit) - 1;

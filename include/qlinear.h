@@ -389,9 +389,8 @@ QL_API ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_sca
    Neither is read on the host, so the call does not synchronize and can be
    captured; replays follow the values that they then hold.  Rows of Y outside
    every segment are left as they are.  An offset outside [0, T] counts as the
-   nearer end and a descending pair as an empty segment (where that makes
-   segments overlap, rows inside segments are unspecified); a source row
-   outside [0, rows_a) gives a row of zeros.  Y must not overlap an operand.
+   nearer end, and one below an earlier offset as that offset (an empty
+   segment); a source row outside [0, rows_a) gives a row of zeros.  Y must not overlap an operand.
    4-byte aligned offsets and row_index; one launch, no workspace. */
 QL_API size_t qlinear_experts_bytes(int32_t E, int32_t N, int32_t K);
 QL_API size_t qlinear_prepare_experts_ws_bytes(int32_t E, int32_t N, int32_t K);

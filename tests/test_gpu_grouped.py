@@ -44,9 +44,9 @@ def _check(ql, q, off, w, y, rows=None, before=0.25, hadamard=True):
     want = torch.full(y.shape, before, dtype=torch.float64, device="cuda")
     bound = torch.zeros_like(want)
     rel = (w.K / 16 + 64) * 2.0 ** -22
-    off = [min(max(int(o), 0), T) for o in off.tolist()]
+    off = np.maximum.accumulate([min(max(int(o), 0), T) for o in off.tolist()])
     for e in range(w.E):
-        lo, hi = off[e], max(off[e], off[e + 1])
+        lo, hi = int(off[e]), int(off[e + 1])
         if hi == lo:
             continue
         pw = w.expert(e)
@@ -152,7 +152,7 @@ def test_offsets_and_rows_out_of_range(ql, total):
     rows[::5] = torch.tensor([-1, 10, 2 ** 31 - 1, -2 ** 31], dtype=torch.int64).to(torch.int32).cuda().repeat(total)[
         :rows[::5].numel()]
     for off in ([-5, 3, 3, total // 2, total + 100], [2 ** 31 - 1] * 5, [-2 ** 31] * 5, [0, 0, 0, 0, 2 ** 31 - 1],
-                [2, total // 2, 1, 1, 1]):
+                [2, total // 2, 1, 1, 1], [0, total, 0, total, 0]):
         y = torch.full((total, 64), 0.25, dtype=torch.bfloat16, device="cuda")
         o = torch.tensor(off, dtype=torch.int64).to(torch.int32).cuda()
         ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, o, w, rows=rows, Y=y)
@@ -216,6 +216,23 @@ def test_a_decoder_block_in_one_graph(ql, tokens):
     assert torch.equal(got[1], want[1])
     assert ql.qlinear_device_status() == 0
     del graphs
+
+
+def test_a_wait_that_runs_out_is_reported(ql):
+    w, _ = _experts(ql, 3, 512, 1920, 16)
+    q = _tokens(ql, 600, 1920, 17)
+    off = _offsets([200, 150, 250])
+    for rows in (None, torch.arange(600, dtype=torch.int32, device="cuda")):
+        want = ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, off, w, rows=rows)
+        torch.cuda.synchronize()
+        ql.qlinear_debug_set_wait_limit(0)
+        try:
+            ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, off, w, rows=rows)
+            torch.cuda.synchronize()
+        finally:
+            ql.qlinear_debug_set_wait_limit(-1)
+        assert ql.qlinear_device_status() == 5 and ql.qlinear_device_status() == 0
+        assert torch.equal(ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, off, w, rows=rows), want)
 
 
 def test_checkpoint(ql):
