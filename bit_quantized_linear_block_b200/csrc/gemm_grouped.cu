@@ -21,11 +21,11 @@
 // stored boxes follow its height.
 //
 // Persistent, one CTA per SM, warps by role:
-//   warp 0      TMA producer: the activation tile (64-row boxes, or
-//               four-row gathers through `rows`; 128-byte swizzle), the FP4
-//               weight tile and its scales, into an RS-deep ring of 64-deep
-//               K stages;
+//   warp 0      weight producer: 256-deep K chunks of the FP4 tile (128-byte
+//               rows, 128-byte swizzle) and their scales by TMA, WS-deep ring;
 //   warp 1      TMEM allocator and MMA issuer (kind::f16, A from tensor memory);
+//   warp 2      activation producer: 64-deep K stages, TMA boxes of 64 rows
+//               or one of BMT, RS-deep ring;
 //   4 XG warps  transform: group g widens the stages with it % XG == g, lane
 //               l of lane quarter q its weight row 32 q + l, into one of AS
 //               32-column slots of tensor memory;
@@ -33,7 +33,18 @@
 //               scale, bf16, and a TMA store of the 32 x 32 box through the
 //               warp's own staging buffer.  A box that reaches past its
 //               segment is stored row by row, so no row of another segment
-//               or behind the last one is written.
+//               or behind the last one is written;
+//   4 warps     (GATHER) activation producers in place of warp 2: 16-byte
+//               asynchronous copies of the rows that `rows` names, into the
+//               same swizzled tile.  (Four-row TMA gathers were slower: 48 a
+//               stage took 1650 cycles or more from three issuing warps,
+//               against 384 cycles of MMA.)
+// Issue is what bounds the producers: a TMA instruction costs its thread
+// about a hundred cycles here, and each box row is a request.  So one lane
+// picked by elect.sync issues (behind `lane == 0` an instruction took about
+// 200 cycles more: 711 against 497 us at five per stage, 17664 x 7680 x
+// 1920), the weights come four stages at a time, and weights and activations
+// have a warp each.
 // All waits are bounded; on a timeout a role records it, drains its own
 // copies or MMAs and leaves the loop, and the CTA frees its tensor memory.
 #include "ql_common.cuh"
@@ -46,6 +57,7 @@ namespace ql {
 constexpr int kMaxExperts = 1024;
 
 struct GroupedArgs {
+  const uint8_t* x;          // f16 codes [rows_a, K]
   const int32_t* offsets;
   const int32_t* rows;       // null: row r of Y is row r of the activations
   const float* row_scale;    // [rows_a]
@@ -61,28 +73,32 @@ struct GroupedArgs {
   int* status;
 };
 
-template <int BMT, int RS, int XG>
+template <int BMT, int RS, int WS, int XG, bool GATHER>
 struct GroupedCfg {
-  static constexpr int BK = 64;
+  static constexpr int BK = 64;                    // K elements of an activation stage
+  static constexpr int WK = 4;                     // stages of a weight chunk
   static constexpr int NACC = (2 * BMT + 4 * 32 <= 512) ? 2 : 1;
   static constexpr int AS = (512 - NACC * BMT) / 32 < 8 ? (512 - NACC * BMT) / 32 : 8;   // A slots
   static constexpr int B_BYTES = BMT * BK * 2;
-  static constexpr int W_BYTES = 128 * BK / 2;
-  static constexpr int SF_BYTES = 512;
+  static constexpr int W_BYTES = 128 * WK * BK / 2;
+  static constexpr int SF_BYTES = WK * 512;
   static constexpr int OFF_B = 0;
   static constexpr int OFF_W = OFF_B + RS * B_BYTES;
-  static constexpr int OFF_SF = OFF_W + RS * W_BYTES;
-  static constexpr int OFF_C = OFF_SF + RS * SF_BYTES;
-  static constexpr int OFF_TAB = OFF_C + 8 * 2 * kWarpBoxBytes;      // first tile, first row, rows of each expert
-  static constexpr int OFF_BAR = OFF_TAB + 3 * 4 * (kMaxExperts + 4);
-  static constexpr int NBAR = 2 * RS + 2 * AS + 2 * 2 + 1;
+  static constexpr int OFF_SF = OFF_W + WS * W_BYTES;
+  static constexpr int OFF_C = OFF_SF + WS * SF_BYTES;
+  static constexpr int OFF_TAB = OFF_C + 8 * 2 * kWarpBoxBytes;      // first tile and first row of each expert
+  static constexpr int OFF_BAR = OFF_TAB + 2 * 4 * (kMaxExperts + 4);
+  static constexpr int NBAR = 2 * RS + 2 * WS + 2 * AS + 2 * 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static constexpr int EPI0 = 4 + 4 * XG;
-  static constexpr int THREADS = (EPI0 + 8) * 32;
+  static constexpr int GAT0 = EPI0 + 8;
+  static constexpr int THREADS = (GAT0 + (GATHER ? 4 : 0)) * 32;
+  static constexpr int LAG = RS / 2 + 1;           // gathered stages in flight per thread
   static_assert(XG >= 1 && XG <= 3, "transform warp groups");
   static_assert(AS >= 2, "tensor memory budget");
-  static_assert(BMT % 64 == 0, "whole activation boxes");
+  static_assert(BMT % 64 == 0 && B_BYTES % 1024 == 0, "whole activation boxes");
+  static_assert(LAG < RS, "a gathered stage is handed over before its slot is needed again");
   static_assert(OFF_BAR % 8 == 0, "mbarrier alignment");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -92,14 +108,16 @@ __device__ __forceinline__ uint32_t grouped_idesc(int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
-// Four rows of a 2-D tensor (one 128-byte piece each) to consecutive
-// 128-byte rows of shared memory.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int4 r) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
-      : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
 struct GroupedTile {
@@ -111,13 +129,12 @@ struct GroupedTile {
 // Walks the tile table in ascending tile order.
 struct TileCursor {
   const int* first;   // first row tile of each expert, [E] the total
-  const int* lo;
-  const int* cnt;
+  const int* lo;      // first row of each expert, [E] the end
   int e;
   __device__ __forceinline__ GroupedTile at(int t, int tiles_n, int bmt) {
     const int tt = t / tiles_n;
     while (first[e + 1] <= tt) ++e;
-    const int count = cnt[e], nt = first[e + 1] - first[e];
+    const int count = lo[e + 1] - lo[e], nt = first[e + 1] - first[e];
     const int per = ((count + nt - 1) / nt + 15) & ~15;
     const int start = (tt - first[e]) * per;
     GroupedTile r;
@@ -139,16 +156,19 @@ __device__ __forceinline__ bool warp_wait_pair(uint64_t* a, uint32_t pa, uint64_
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-template <int BMT, int RS, int XG>
-__global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
-    k_gemm_grouped(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                   const __grid_constant__ CUtensorMap tm_y, const GroupedArgs p) {
-  using C = GroupedCfg<BMT, RS, XG>;
+template <int BMT, int RS, int WS, int XG, bool GATHER>
+__global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG, GATHER>::THREADS, 1)
+    k_gemm_grouped(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xw,
+                   const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_y,
+                   const GroupedArgs p) {
+  using C = GroupedCfg<BMT, RS, WS, XG, GATHER>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* raw_empty = raw_full + RS;
-  uint64_t* xf_full = raw_empty + RS;
+  uint64_t* b_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* b_empty = b_full + RS;
+  uint64_t* w_full = b_empty + RS;
+  uint64_t* w_empty = w_full + WS;
+  uint64_t* xf_full = w_empty + WS;
   uint64_t* xf_empty = xf_full + C::AS;
   uint64_t* tfull = xf_empty + C::AS;
   uint64_t* tempty = tfull + 2;
@@ -157,17 +177,23 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* s_first = reinterpret_cast<int*>(smem + C::OFF_TAB);
   int* s_lo = s_first + kMaxExperts + 4;
-  int* s_cnt = s_lo + kMaxExperts + 4;
 
   const int warp = threadIdx.x >> 5;
   const uint32_t lane = lane_id();
   if (threadIdx.x == 0) {
-    prefetch_tmap(&tm_x);
+    if (!GATHER) {
+      prefetch_tmap(&tm_x);
+      prefetch_tmap(&tm_xw);
+    }
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_y);
     for (int i = 0; i < RS; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 1);
+      mbar_init(&b_full[i], GATHER ? 4 : 1);   // the gathering warps, or the TMA's byte count
+      mbar_init(&b_empty[i], 1);
+    }
+    for (int i = 0; i < WS; ++i) {
+      mbar_init(&w_full[i], 1);
+      mbar_init(&w_empty[i], 4 * C::WK);       // four transform warps x the chunk's stages
     }
     for (int i = 0; i < C::AS; ++i) {
       mbar_init(&xf_full[i], 4);
@@ -195,11 +221,13 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
       if (e < p.E) {
         s_first[e] = total + end - tiles;
         s_lo[e] = static_cast<int>(lo);
-        s_cnt[e] = cnt;
       }
       total += __shfl_sync(0xffffffffu, end, 31);
     }
-    if (lane == 0) s_first[p.E] = total;
+    if (lane == 0) {
+      s_first[p.E] = total;
+      s_lo[p.E] = static_cast<int>(carry);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -207,64 +235,107 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t a_slots = tmem + C::NACC * BMT;
   const int num_tiles = s_first[p.E] * p.tiles_n;
-  TileCursor cur{s_first, s_lo, s_cnt, 0};
+  TileCursor cur{s_first, s_lo, 0};
+  const int chunks = (p.num_kst + C::WK - 1) / C::WK;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    int it = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-      const GroupedTile g = cur.at(t, p.tiles_n, BMT);
-      const int boxes = (g.n + 63) >> 6;
-      int4 src[2];   // gathers: source rows of four-row groups lane and lane + 32
-      if (p.rows != nullptr) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int r[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // rows past the tile's last repeat it; a row that does not exist
-            // reads row 0 and gets scale 0 in the epilogue
-            const int m = min(4 * (static_cast<int>(lane) + 32 * h) + i, g.rows - 1);
-            const int v = p.rows[static_cast<int64_t>(g.row0) + m];
-            r[i] = v >= 0 && v < p.rows_a ? v : 0;
+    // ------------------------------------------------------------ weight producer
+    if (elect_one()) {
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+        const GroupedTile g = cur.at(t, p.tiles_n, BMT);
+        const uint8_t* sf = p.sf + static_cast<size_t>(g.e) * p.expert_sf + static_cast<size_t>(g.nb) * p.k_atoms * 512;
+        const int wrow = g.e * p.N + g.nb * 128;
+        for (int c = 0; c < chunks; ++c, ++it) {
+          const int s = it % WS;
+          if (*abort_flag || !mbar_wait(&w_empty[s], ((it / WS) & 1) ^ 1, p.wait_limit)) {
+            ok = false;
+            break;
           }
-          src[h] = make_int4(r[0], r[1], r[2], r[3]);
+          const uint32_t sf_bytes = 512 * min(C::WK, p.num_kst - C::WK * c);
+          mbar_arrive_expect_tx(&w_full[s], C::W_BYTES + sf_bytes);
+          tma_load_2d(smem + C::OFF_W + s * C::W_BYTES, &tm_w, &w_full[s], c * (C::WK * C::BK / 2), wrow);
+          bulk_load(smem + C::OFF_SF + s * C::SF_BYTES, sf + static_cast<size_t>(c) * C::SF_BYTES, sf_bytes, &w_full[s]);
         }
       }
-      const uint8_t* sf = p.sf + static_cast<size_t>(g.e) * p.expert_sf + static_cast<size_t>(g.nb) * p.k_atoms * 512;
-      const int wrow = g.e * p.N + g.nb * 128;
-      for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
+      if (!ok) fail_timeout(p.status, abort_flag);
+      drain_loads(w_full, it, WS, p.status);
+    }
+  } else if (warp == 2 && !GATHER) {
+    // ------------------------------------------------------------ activation producer
+    if (elect_one()) {
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+        const GroupedTile g = cur.at(t, p.tiles_n, BMT);
+        const int boxes = g.n > 128 ? 0 : (g.n + 63) >> 6;     // 0: one box of BMT rows
+        const uint32_t bytes = g.n > 128 ? C::B_BYTES : 8192 * boxes;
+        for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
+          const int s = it % RS;
+          if (*abort_flag || !mbar_wait(&b_empty[s], ((it / RS) & 1) ^ 1, p.wait_limit)) {
+            ok = false;
+            break;
+          }
+          uint8_t* b = smem + C::OFF_B + s * C::B_BYTES;
+          mbar_arrive_expect_tx(&b_full[s], bytes);
+          if (boxes == 0) tma_load_2d(b, &tm_xw, &b_full[s], ks * C::BK, g.row0);
+          for (int i = 0; i < boxes; ++i) tma_load_2d(b + i * 8192, &tm_x, &b_full[s], ks * C::BK, g.row0 + 64 * i);
+        }
+      }
+      if (!ok) fail_timeout(p.status, abort_flag);
+      drain_loads(b_full, it, RS, p.status);
+    }
+  } else if (GATHER && warp >= C::GAT0) {
+    // ------------------------------------------------------------ gathering producers
+    // Thread (r, c) of 16 x 8 copies 16-byte piece c of rows r, r + 16, ...
+    // of the tile.  A stage is handed to the MMA once this thread's copies of
+    // it have landed, LAG stages later.
+    const int tid = static_cast<int>(threadIdx.x) - 32 * C::GAT0;
+    const int r = tid >> 3, c = tid & 7;
+    const uint32_t dst0 = smem_u32(smem + C::OFF_B) + r * 128 + ((c ^ (r & 7)) << 4);
+    int it = 0;
+    bool ok = true;
+    auto hand_over = [&](int stage) {
+      fence_proxy_async_smem();      // the copies' writes before the MMA's reads
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_full[stage % RS]);
+    };
+    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+      const GroupedTile g = cur.at(t, p.tiles_n, BMT);
+      const int steps = g.n >> 4;
+      int src[BMT / 16];
+#pragma unroll
+      for (int i = 0; i < BMT / 16; ++i) {
+        // rows past the tile's last repeat it; a row that does not exist
+        // reads row 0 and gets scale 0 in the epilogue
+        const int v = p.rows[static_cast<int64_t>(g.row0) + min(r + 16 * i, g.rows - 1)];
+        src[i] = v >= 0 && v < p.rows_a ? v : 0;
+      }
+      const uint8_t* x = p.x + 16 * c;
+      const size_t pitch = static_cast<size_t>(p.K) * 2;
+      for (int ks = 0; ks < p.num_kst; ++ks, ++it, x += 128) {
         const int s = it % RS;
-        if (!warp_wait_pair(&raw_empty[s], ((it / RS) & 1) ^ 1, nullptr, 0, p.wait_limit, abort_flag)) {
+        if (!warp_wait_pair(&b_empty[s], ((it / RS) & 1) ^ 1, nullptr, 0, p.wait_limit, abort_flag)) {
           ok = false;
           break;
         }
-        uint8_t* b = smem + C::OFF_B + s * C::B_BYTES;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&raw_full[s],
-                                (p.rows != nullptr ? g.n * 128 : boxes * 8192) + C::W_BYTES + C::SF_BYTES);
-          tma_load_2d(smem + C::OFF_W + s * C::W_BYTES, &tm_w, &raw_full[s], ks * (C::BK / 2), wrow);
-          bulk_load(smem + C::OFF_SF + s * C::SF_BYTES, sf + static_cast<size_t>(ks) * 512, C::SF_BYTES, &raw_full[s]);
-          if (p.rows == nullptr)
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(b + i * 8192, &tm_x, &raw_full[s], ks * C::BK, g.row0 + 64 * i);
-        }
-        if (p.rows != nullptr) {
-          __syncwarp();   // the byte count is set before any gather can complete
+        const uint32_t dst = dst0 + s * C::B_BYTES;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int i = static_cast<int>(lane) + 32 * h;
-            if (4 * i < g.n) tma_gather4(b + i * 512, &tm_x, &raw_full[s], ks * C::BK, src[h]);
-          }
+        for (int i = 0; i < BMT / 16; ++i)
+          if (i < steps) cp_async16(dst + i * 2048, x + src[i] * pitch);
+        cp_async_commit();
+        if (it >= C::LAG) {
+          cp_async_wait<C::LAG>();
+          hand_over(it - C::LAG);
         }
       }
     }
-    if (lane == 0) {
-      if (!ok) fail_timeout(p.status, abort_flag);
-      drain_loads(raw_full, it, RS, p.status);
-    }
-    __syncwarp();
+    cp_async_wait<0>();
+    if (ok)
+      for (int stage = max(0, it - C::LAG); stage < it; ++stage) hand_over(stage);
+    else if (lane == 0)
+      fail_timeout(p.status, abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
@@ -281,7 +352,7 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
         const uint32_t d_tmem = tmem + acc * BMT;
         for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
           const int rs = it % RS, sl = it % C::AS;
-          if (*abort_flag || !mbar_wait(&raw_full[rs], (it / RS) & 1, p.wait_limit) ||
+          if (*abort_flag || !mbar_wait(&b_full[rs], (it / RS) & 1, p.wait_limit) ||
               !mbar_wait(&xf_full[sl], (it / C::AS) & 1, p.wait_limit)) {
             ok = false;
             break;
@@ -292,7 +363,7 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
           for (int i = 0; i < C::BK / 16; ++i)
             tc_mma_f16_ts(d_tmem, a_slots + 32 * sl + 8 * i, smem_desc(b_base + 32 * i, 0, 1024, kSwizzle128B), idesc,
                           (ks > 0 || i > 0) ? 1u : 0u);
-          tc_commit(&raw_empty[rs]);
+          tc_commit(&b_empty[rs]);
           tc_commit(&xf_empty[sl]);
         }
         if (!ok) break;
@@ -306,22 +377,25 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
     const uint32_t q = static_cast<uint32_t>(warp & 3);
     const uint32_t row = 32 * q + lane;
     const int group = (warp - 4) >> 2;
-    int it = 0;
+    int it0 = 0, chunk0 = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-      for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
-        if (it % XG != group) continue;
-        const int rs = it % RS, sl = it % C::AS;
-        if (!warp_wait_pair(&raw_full[rs], (it / RS) & 1, &xf_empty[sl], ((it / C::AS) & 1) ^ 1, p.wait_limit,
+    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, it0 += p.num_kst, chunk0 += chunks) {
+      for (int ks = (group + XG - it0 % XG) % XG; ks < p.num_kst; ks += XG) {
+        const int it = it0 + ks, sl = it % C::AS;
+        const int chunk = chunk0 + ks / C::WK, ws = chunk % WS, sub = ks % C::WK;
+        if (!warp_wait_pair(&w_full[ws], (chunk / WS) & 1, &xf_empty[sl], ((it / C::AS) & 1) ^ 1, p.wait_limit,
                             abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
         // scale atom: byte (row % 32) * 16 + (row / 32) * 4 + k16 holds the block scale of K block k16
-        const uint32_t sb4 = *reinterpret_cast<const uint32_t*>(smem + C::OFF_SF + rs * C::SF_BYTES + lane * 16 + q * 4);
-        const uint4* wr = reinterpret_cast<const uint4*>(smem + C::OFF_W + rs * C::W_BYTES + row * 32);
-        const uint4 c0 = wr[0], c1 = wr[1];
+        const uint32_t sb4 = *reinterpret_cast<const uint32_t*>(smem + C::OFF_SF + ws * C::SF_BYTES + sub * 512 +
+                                                                lane * 16 + q * 4);
+        // 16-byte piece i of a swizzled 128-byte row sits at i ^ (row % 8)
+        const uint8_t* wr = smem + C::OFF_W + ws * C::W_BYTES + row * 128;
+        const uint4 c0 = *reinterpret_cast<const uint4*>(wr + (((2 * sub) ^ (row & 7)) << 4));
+        const uint4 c1 = *reinterpret_cast<const uint4*>(wr + (((2 * sub + 1) ^ (row & 7)) << 4));
         const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
         uint32_t v[32];
 #pragma unroll
@@ -336,7 +410,12 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&xf_full[sl]);
+        if (lane == 0) {
+          mbar_arrive(&xf_full[sl]);
+          // a chunk of two stages (the last one of some K) counts each twice
+          mbar_arrive_n(&w_empty[ws], p.num_kst - ks / C::WK * C::WK >= C::WK ? 1 : 2);
+        }
+        __syncwarp();   // the tcgen05 instructions need the whole warp together
       }
     }
     if (!ok && lane == 0) fail_timeout(p.status, abort_flag);
@@ -355,8 +434,6 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
       const int n0 = g.nb * 128 + 32 * static_cast<int>(q);
       const int boxes = n0 < p.N ? (g.rows + 31) >> 5 : 0;       // this warp's: half, half + 2, ...
       for (int c = half; c < boxes; c += 2) {
-        uint32_t r[32];
-        tmem_ld32(tmem + ((32 * q) << 16) + acc * BMT + 32 * c, r);
         const int m = 32 * c + static_cast<int>(lane);           // row of the tile
         float a_l = 0.f;
         if (m < g.rows) {
@@ -364,6 +441,9 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
           if (p.rows != nullptr) src = p.rows[src];
           if (src >= 0 && src < p.rows_a) a_l = __fmul_rn(alpha, ld_dep(p.row_scale + src));
         }
+        uint32_t r[32];
+        __syncwarp();   // the tcgen05 instructions need the whole warp together
+        tmem_ld32(tmem + ((32 * q) << 16) + acc * BMT + 32 * c, r);
         tmem_ld_wait();
         if (c + 2 >= boxes) {
           tc_fence_before();
@@ -410,23 +490,26 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, XG>::THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int BMT, int RS, int XG>
+template <int BMT, int RS, int WS, int XG, bool GATHER>
 static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                                     const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
                                     int* status) {
-  using C = GroupedCfg<BMT, RS, XG>;
+  using C = GroupedCfg<BMT, RS, WS, XG, GATHER>;
   const int N = w->N, K = w->K;
-  CUtensorMap tx, tw, ty;
-  if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows_a, static_cast<int64_t>(K) * 2, C::BK,
-                    rows != nullptr ? 1 : 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+  CUtensorMap tx, txw, tw, ty;
+  if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows_a, static_cast<int64_t>(K) * 2, C::BK, 64,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&txw, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows_a, static_cast<int64_t>(K) * 2, C::BK, BMT,
+                    CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, static_cast<int64_t>(w->E) * N, K / 2,
-                    C::BK / 2, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                    C::WK * C::BK / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, T, static_cast<int64_t>(N) * 2, 32, 32,
                     CU_TENSOR_MAP_SWIZZLE_NONE))
     return QL_ERR_CUDA;
   GroupedArgs p{};
   GemmArgs limits{};
   fill_gemm_args(limits, T, N, K, 128, status);
+  p.x = static_cast<const uint8_t*>(a);
   p.offsets = offsets;
   p.rows = rows;
   p.row_scale = a_scales;
@@ -449,10 +532,10 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   const int64_t e = std::min<int64_t>(w->E, T);
   const int64_t tiles = (e + (T - e) / BMT) * p.tiles_n;
   if (tiles > 0x7FFFFFFF - num_sms()) return QL_ERR_UNSUPPORTED_SHAPE;
-  auto kern = k_gemm_grouped<BMT, RS, XG>;
+  auto kern = k_gemm_grouped<BMT, RS, WS, XG, GATHER>;
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return QL_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(tiles, num_sms()));
-  if (launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, st, 1, tx, tw, ty, p) != cudaSuccess) {
+  if (launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, st, 1, tx, txw, tw, ty, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return QL_ERR_CUDA;
   }
@@ -462,7 +545,9 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
 ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                               const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
                               int* status) {
-  return launch_grouped_cfg<192, 6, 2>(a, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+  if (rows != nullptr)
+    return launch_grouped_cfg<192, 6, 2, 2, true>(a, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+  return launch_grouped_cfg<192, 6, 2, 2, false>(a, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
 }
 
 }  // namespace ql
