@@ -705,9 +705,20 @@ ql_status qlinear_prepare_experts(const void* W, int32_t E, int32_t N, int32_t K
   return QL_OK;
 }
 
+namespace {
+// Few rows per expert: the weights' bytes are the whole cost, and the form
+// that streams them needs no tensor-memory tiles.
+bool grouped_few(int64_t T, int64_t E) { return T <= 16 || T <= 4 * E; }
+}  // namespace
+
+size_t qlinear_grouped_gemm_ws_bytes(int64_t T, const ql_experts* w, int32_t gathers) {
+  if (T <= 0 || w == nullptr || check_m(T) != QL_OK || check_experts_shape(w->E, w->N, w->K) != QL_OK) return 0;
+  return gathers && !grouped_few(T, w->E) ? align256(static_cast<size_t>(T) * w->K * 2) : 0;
+}
+
 ql_status qlinear_grouped_gemm(int32_t act_fmt, const void* a_codes, const float* a_scales, int64_t rows_a,
                                const int32_t* row_index, const int32_t* offsets, int64_t T, const ql_experts* w,
-                               void* Y, void* stream) {
+                               void* Y, void* ws, size_t ws_bytes, void* stream) {
   QL_TRY(check_m(T));
   QL_TRY(check_m(rows_a));
   if (w == nullptr || w->codes == nullptr || w->sf == nullptr || w->gscale == nullptr) return QL_ERR_INVALID_ARG;
@@ -717,14 +728,16 @@ ql_status qlinear_grouped_gemm(int32_t act_fmt, const void* a_codes, const float
   if (T > 0 && (a_codes == nullptr || a_scales == nullptr || offsets == nullptr || Y == nullptr || rows_a == 0))
     return QL_ERR_INVALID_ARG;
   if (!aligned(a_codes, 16) || !aligned(Y, 16) || !aligned(a_scales, 4) || !aligned(row_index, 4) ||
-      !aligned(offsets, 4))
+      !aligned(offsets, 4) || !aligned(ws, 256))
     return QL_ERR_ALIGNMENT;
+  const size_t need = qlinear_grouped_gemm_ws_bytes(T, w, row_index != nullptr);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return QL_ERR_WORKSPACE;
   QL_TRY(device_ready());
   if (T == 0) return QL_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (T <= 16 || T <= 4 * static_cast<int64_t>(w->E))
+  if (grouped_few(T, w->E))
     return launch_grouped_few(a_codes, a_scales, rows_a, row_index, offsets, T, w, Y, st);
-  return launch_gemm_grouped(a_codes, a_scales, rows_a, row_index, offsets, T, w, Y, st, status_word());
+  return launch_gemm_grouped(a_codes, a_scales, rows_a, row_index, offsets, T, w, Y, ws, st, status_word());
 }
 
 // ---------------------------------------------------------------- forward

@@ -33,12 +33,7 @@
 //               scale, bf16, and a TMA store of the 32 x 32 box through the
 //               warp's own staging buffer.  A box that reaches past its
 //               segment is stored row by row, so no row of another segment
-//               or behind the last one is written;
-//   4 warps     (GATHER) activation producers in place of warp 2: 16-byte
-//               asynchronous copies of the rows that `rows` names, into the
-//               same swizzled tile.  (Four-row TMA gathers were slower: 48 a
-//               stage took 1650 cycles or more from three issuing warps,
-//               against 384 cycles of MMA.)
+//               or behind the last one is written.
 // Issue is what bounds the producers: a TMA instruction costs its thread
 // about a hundred cycles here, and each box row is a request.  So one lane
 // picked by elect.sync issues (behind `lane == 0` an instruction took about
@@ -57,15 +52,14 @@ namespace ql {
 constexpr int kMaxExperts = 1024;
 
 struct GroupedArgs {
-  const uint8_t* x;          // f16 codes [rows_a, K]
   const int32_t* offsets;
-  const int32_t* rows;       // null: row r of Y is row r of the activations
+  const int32_t* rows;       // scale of row r: row_scale[rows[r]]; null: row_scale[r]
   const float* row_scale;    // [rows_a]
   const float* g_w;          // [E]
   const uint8_t* sf;
   __nv_bfloat16* y;
   size_t expert_sf;
-  int64_t rows_a, T;
+  int64_t rows_a, T;         // rows of row_scale, of Y
   int32_t E, N, K;
   int32_t tiles_n, num_kst, k_atoms;
   float alpha_mul;
@@ -73,7 +67,7 @@ struct GroupedArgs {
   int* status;
 };
 
-template <int BMT, int RS, int WS, int XG, bool GATHER>
+template <int BMT, int RS, int WS, int XG>
 struct GroupedCfg {
   static constexpr int BK = 64;                    // K elements of an activation stage
   static constexpr int WK = 4;                     // stages of a weight chunk
@@ -92,13 +86,10 @@ struct GroupedCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static constexpr int EPI0 = 4 + 4 * XG;
-  static constexpr int GAT0 = EPI0 + 8;
-  static constexpr int THREADS = (GAT0 + (GATHER ? 4 : 0)) * 32;
-  static constexpr int LAG = RS / 2 + 1;           // gathered stages in flight per thread
+  static constexpr int THREADS = (EPI0 + 8) * 32;
   static_assert(XG >= 1 && XG <= 3, "transform warp groups");
   static_assert(AS >= 2, "tensor memory budget");
   static_assert(BMT % 64 == 0 && B_BYTES % 1024 == 0, "whole activation boxes");
-  static_assert(LAG < RS, "a gathered stage is handed over before its slot is needed again");
   static_assert(OFF_BAR % 8 == 0, "mbarrier alignment");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -108,14 +99,6 @@ __device__ __forceinline__ uint32_t grouped_idesc(int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
@@ -156,12 +139,12 @@ __device__ __forceinline__ bool warp_wait_pair(uint64_t* a, uint32_t pa, uint64_
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-template <int BMT, int RS, int WS, int XG, bool GATHER>
-__global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG, GATHER>::THREADS, 1)
+template <int BMT, int RS, int WS, int XG>
+__global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
     k_gemm_grouped(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xw,
                    const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_y,
                    const GroupedArgs p) {
-  using C = GroupedCfg<BMT, RS, WS, XG, GATHER>;
+  using C = GroupedCfg<BMT, RS, WS, XG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
   uint64_t* b_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -181,14 +164,12 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG, GATHER>::THREADS, 
   const int warp = threadIdx.x >> 5;
   const uint32_t lane = lane_id();
   if (threadIdx.x == 0) {
-    if (!GATHER) {
-      prefetch_tmap(&tm_x);
-      prefetch_tmap(&tm_xw);
-    }
+    prefetch_tmap(&tm_x);
+    prefetch_tmap(&tm_xw);
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_y);
     for (int i = 0; i < RS; ++i) {
-      mbar_init(&b_full[i], GATHER ? 4 : 1);   // the gathering warps, or the TMA's byte count
+      mbar_init(&b_full[i], 1);
       mbar_init(&b_empty[i], 1);
     }
     for (int i = 0; i < WS; ++i) {
@@ -262,7 +243,7 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG, GATHER>::THREADS, 
       if (!ok) fail_timeout(p.status, abort_flag);
       drain_loads(w_full, it, WS, p.status);
     }
-  } else if (warp == 2 && !GATHER) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------ activation producer
     if (elect_one()) {
       int it = 0;
@@ -286,56 +267,6 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG, GATHER>::THREADS, 
       if (!ok) fail_timeout(p.status, abort_flag);
       drain_loads(b_full, it, RS, p.status);
     }
-  } else if (GATHER && warp >= C::GAT0) {
-    // ------------------------------------------------------------ gathering producers
-    // Thread (r, c) of 16 x 8 copies 16-byte piece c of rows r, r + 16, ...
-    // of the tile.  A stage is handed to the MMA once this thread's copies of
-    // it have landed, LAG stages later.
-    const int tid = static_cast<int>(threadIdx.x) - 32 * C::GAT0;
-    const int r = tid >> 3, c = tid & 7;
-    const uint32_t dst0 = smem_u32(smem + C::OFF_B) + r * 128 + ((c ^ (r & 7)) << 4);
-    int it = 0;
-    bool ok = true;
-    auto hand_over = [&](int stage) {
-      fence_proxy_async_smem();      // the copies' writes before the MMA's reads
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b_full[stage % RS]);
-    };
-    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-      const GroupedTile g = cur.at(t, p.tiles_n, BMT);
-      const int steps = g.n >> 4;
-      int src[BMT / 16];
-#pragma unroll
-      for (int i = 0; i < BMT / 16; ++i) {
-        // rows past the tile's last repeat it; a row that does not exist
-        // reads row 0 and gets scale 0 in the epilogue
-        const int v = p.rows[static_cast<int64_t>(g.row0) + min(r + 16 * i, g.rows - 1)];
-        src[i] = v >= 0 && v < p.rows_a ? v : 0;
-      }
-      const uint8_t* x = p.x + 16 * c;
-      const size_t pitch = static_cast<size_t>(p.K) * 2;
-      for (int ks = 0; ks < p.num_kst; ++ks, ++it, x += 128) {
-        const int s = it % RS;
-        if (!warp_wait_pair(&b_empty[s], ((it / RS) & 1) ^ 1, nullptr, 0, p.wait_limit, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = dst0 + s * C::B_BYTES;
-#pragma unroll
-        for (int i = 0; i < BMT / 16; ++i)
-          if (i < steps) cp_async16(dst + i * 2048, x + src[i] * pitch);
-        cp_async_commit();
-        if (it >= C::LAG) {
-          cp_async_wait<C::LAG>();
-          hand_over(it - C::LAG);
-        }
-      }
-    }
-    cp_async_wait<0>();
-    if (ok)
-      for (int stage = max(0, it - C::LAG); stage < it; ++stage) hand_over(stage);
-    else if (lane == 0)
-      fail_timeout(p.status, abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
@@ -490,16 +421,16 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG, GATHER>::THREADS, 
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int BMT, int RS, int WS, int XG, bool GATHER>
+template <int BMT, int RS, int WS, int XG>
 static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                                     const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
                                     int* status) {
-  using C = GroupedCfg<BMT, RS, WS, XG, GATHER>;
+  using C = GroupedCfg<BMT, RS, WS, XG>;
   const int N = w->N, K = w->K;
   CUtensorMap tx, txw, tw, ty;
-  if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows_a, static_cast<int64_t>(K) * 2, C::BK, 64,
+  if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows != nullptr ? T : rows_a, static_cast<int64_t>(K) * 2, C::BK, 64,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&txw, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows_a, static_cast<int64_t>(K) * 2, C::BK, BMT,
+      !make_tmap_2d(&txw, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows != nullptr ? T : rows_a, static_cast<int64_t>(K) * 2, C::BK, BMT,
                     CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, static_cast<int64_t>(w->E) * N, K / 2,
                     C::WK * C::BK / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -509,7 +440,6 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   GroupedArgs p{};
   GemmArgs limits{};
   fill_gemm_args(limits, T, N, K, 128, status);
-  p.x = static_cast<const uint8_t*>(a);
   p.offsets = offsets;
   p.rows = rows;
   p.row_scale = a_scales;
@@ -532,7 +462,7 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   const int64_t e = std::min<int64_t>(w->E, T);
   const int64_t tiles = (e + (T - e) / BMT) * p.tiles_n;
   if (tiles > 0x7FFFFFFF - num_sms()) return QL_ERR_UNSUPPORTED_SHAPE;
-  auto kern = k_gemm_grouped<BMT, RS, WS, XG, GATHER>;
+  auto kern = k_gemm_grouped<BMT, RS, WS, XG>;
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return QL_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(tiles, num_sms()));
   if (launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, st, 1, tx, txw, tw, ty, p) != cudaSuccess) {
@@ -542,12 +472,44 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   return QL_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Source rows into output order: out[r] = a[rows[r]] (row 0 for a row that
+// does not exist: the product scales it by 0).  HBM: 2 bytes per value
+// written, and read where a row is new to L2.  The product then loads whole
+// boxes; gathering inside it was slower, since each row tile is loaded once
+// per 128 columns of Y: 17664 x 7680 x 1920 took 974 us with four-row TMA
+// gathers and 742 us with 16-byte asynchronous copies, against 388 us for
+// rows in order.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kThreadsHbm) k_gather_rows(const uint4* a, const int32_t* rows, int64_t rows_a, int64_t T,
+                                                             int32_t pieces, uint4* out) {
+  pdl_wait();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreadsHbm / 32);
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreadsHbm / 32) + (threadIdx.x >> 5); r < T; r += step) {
+    const int32_t v = rows[r];
+    const uint4* src = a + (v >= 0 && v < rows_a ? v : 0) * static_cast<int64_t>(pieces);
+    uint4* dst = out + r * pieces;
+#pragma unroll 4
+    for (int32_t i = static_cast<int32_t>(lane_id()); i < pieces; i += 32) dst[i] = src[i];
+  }
+  pdl_release();
+}
+
 ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
-                              const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
-                              int* status) {
-  if (rows != nullptr)
-    return launch_grouped_cfg<192, 6, 2, 2, true>(a, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
-  return launch_grouped_cfg<192, 6, 2, 2, false>(a, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+                              const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, void* gathered,
+                              cudaStream_t st, int* status) {
+  const void* x = a;
+  if (rows != nullptr) {
+    const int64_t want = (T + kThreadsHbm / 32 - 1) / (kThreadsHbm / 32);   // a warp per row
+    const int grid = static_cast<int>(std::min<int64_t>(want, 8ll * num_sms()));
+    if (launch_pdl(k_gather_rows, dim3(grid), dim3(kThreadsHbm), 0, st, 1, static_cast<const uint4*>(a), rows, rows_a, T,
+                   w->K / 8, static_cast<uint4*>(gathered)) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return QL_ERR_CUDA;
+    }
+    x = gathered;
+  }
+  return launch_grouped_cfg<192, 6, 2, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
 }
 
 }  // namespace ql

@@ -79,10 +79,11 @@ ql_status launch_gemv(int act, const void* a, const float* a_scales, int64_t M, 
 // The product grouped by expert for few rows per expert (f16 codes); rows may be null.
 ql_status launch_grouped_few(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                              const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st);
-// The same product on tensor-memory tiles, for any number of rows per expert.
+// The same product on tensor-memory tiles; `gathered`: room for [T, K] f16
+// when rows is given.
 ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
-                              const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
-                              int* status);
+                              const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, void* gathered,
+                              cudaStream_t st, int* status);
 ql_status launch_gemm_w4a4(const void* a_codes, const uint8_t* a_sf, const float* g_a, int64_t M,
                            const ql_weights* w, void* Y, cudaStream_t st, int* status, Gate gate = {});
 // a_f16 = 1: activations are f16 [M, K] holding the INT8 codes (needs

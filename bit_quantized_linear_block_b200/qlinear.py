@@ -105,7 +105,8 @@ def _load() -> C.CDLL:
         "qlinear_experts_bytes": (sz, [i32, i32, i32]),
         "qlinear_prepare_experts_ws_bytes": (sz, [i32, i32, i32]),
         "qlinear_prepare_experts": (C.c_int, [vp, i32, i32, i32, i32, vp, sz, C.POINTER(Experts), vp, sz, vp]),
-        "qlinear_grouped_gemm": (C.c_int, [i32, vp, vp, i64, vp, vp, i64, C.POINTER(Experts), vp, vp]),
+        "qlinear_grouped_gemm": (C.c_int, [i32, vp, vp, i64, vp, vp, i64, C.POINTER(Experts), vp, vp, sz, vp]),
+        "qlinear_grouped_gemm_ws_bytes": (sz, [i64, C.POINTER(Experts), i32]),
         "qlinear_forward_ws_bytes": (sz, [i64, C.POINTER(Weights), i32]),
         "qlinear_forward": (C.c_int, [vp, i64, C.POINTER(Weights), i32, vp, vp, sz, vp]),
         "qlinear_forward_routed_ws_bytes": (sz, [i64, C.POINTER(Weights)]),
@@ -640,7 +641,8 @@ def qlinear_prepare_experts(W: torch.Tensor, hadamard: bool = True, stream=None)
 
 
 def qlinear_grouped_gemm(act_fmt: int, q: dict, offsets: torch.Tensor, w: PackedExperts,
-                         rows: torch.Tensor | None = None, Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                         rows: torch.Tensor | None = None, Y: torch.Tensor | None = None,
+                         ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The layer grouped by expert: row r of segment [offsets[e],
     offsets[e+1]) of Y is row `rows[r]` (r without `rows`) of the quantized
     activations times expert e's weights.  `q`: the codes and scales of
@@ -648,7 +650,9 @@ def qlinear_grouped_gemm(act_fmt: int, q: dict, offsets: torch.Tensor, w: Packed
     int32, one per row of Y (a token may appear in many rows).  Y has
     Y.shape[0], rows.numel() or the codes' row count; its rows outside every
     segment are left as they are (unset in a Y made here).  Offsets and rows
-    stay on the device: no synchronization."""
+    stay on the device: no synchronization.  ws: scratch of
+    lib.qlinear_grouped_gemm_ws_bytes(T, w.desc, rows is not None) bytes, made
+    here when not given."""
     if not isinstance(w, PackedExperts):
         raise TypeError(f"w must be PackedExperts (from qlinear_prepare_experts), got {type(w).__name__}")
     if act_fmt not in (QL_ACT_INT8_F16, QL_ACT_INT6_F16):
@@ -669,13 +673,18 @@ def qlinear_grouped_gemm(act_fmt: int, q: dict, offsets: torch.Tensor, w: Packed
         _tensor(Y, "Y", torch.bfloat16, dev, dim=2)
         if Y.shape[1] != w.N or Y.shape[0] != T:
             raise ValueError(f"Y is {tuple(Y.shape)}, the call writes {(T, w.N)}")
+    if ws is not None:
+        _tensor(ws, "ws", torch.uint8, dev)
     st = _stream(stream, dev)
     with _call_on(dev, stream, codes, scales, offsets, rows, w.buf):
         if Y is None:
             Y = torch.empty((T, w.N), dtype=torch.bfloat16, device=dev)
+        if ws is None and rows is not None:
+            need = lib.qlinear_grouped_gemm_ws_bytes(T, C.byref(w.desc), 1)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         _check("qlinear_grouped_gemm",
                lib.qlinear_grouped_gemm(act_fmt, _ptr(codes), _ptr(scales), n_src, _ptr(rows), _ptr(offsets), T,
-                                        C.byref(w.desc), _ptr(Y), st))
+                                        C.byref(w.desc), _ptr(Y), _ptr(ws), 0 if ws is None else ws.numel(), st))
     return Y
 
 

@@ -391,15 +391,19 @@ QL_API ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_sca
    every segment are left as they are.  An offset outside [0, T] counts as the
    nearer end, and one below an earlier offset as that offset (an empty
    segment); a source row outside [0, rows_a) gives a row of zeros.  Y must not overlap an operand.
-   4-byte aligned offsets and row_index; one launch, no workspace. */
+   4-byte aligned offsets and row_index.  ws: qlinear_grouped_gemm_ws_bytes(T,
+   w, row_index != NULL) bytes of scratch (0: ws may be NULL), 256-byte
+   aligned, not initialized; calls in flight at once need one each. */
 QL_API size_t qlinear_experts_bytes(int32_t E, int32_t N, int32_t K);
 QL_API size_t qlinear_prepare_experts_ws_bytes(int32_t E, int32_t N, int32_t K);
 QL_API ql_status qlinear_prepare_experts(const void* W_bf16, int32_t E, int32_t N, int32_t K, int32_t hadamard,
                                          void* wbuf, size_t wbuf_bytes, ql_experts* out, void* ws,
                                          size_t ws_bytes, void* stream);
+QL_API size_t qlinear_grouped_gemm_ws_bytes(int64_t T, const ql_experts* w, int32_t gathers);
 QL_API ql_status qlinear_grouped_gemm(int32_t act_fmt, const void* a_codes, const float* a_scales, int64_t rows_a,
                                       const int32_t* row_index, const int32_t* offsets, int64_t T,
-                                      const ql_experts* w, void* Y_bf16, void* stream);
+                                      const ql_experts* w, void* Y_bf16, void* ws, size_t ws_bytes,
+                                      void* stream);
 
 /* ---- forward: quantize + GEMM ----------------------------------------------
    route: QL_ROUTE_NVFP4, QL_ROUTE_INT8 or QL_ROUTE_INT6 for NVFP4 weights

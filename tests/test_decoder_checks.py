@@ -107,9 +107,10 @@ def test_experts_c_checks(ql):
 
     good = dict(E=4, N=64, K=128, hadamard=1, codes=FAKE[3], sf=FAKE[4], gscale=FAKE[5])
 
-    def f(fmt=ql.QL_ACT_INT8_F16, a=FAKE[0], sc=FAKE[1], n_a=8, rows=None, off=FAKE[2], t=8, w=good, y=FAKE[6]):
+    def f(fmt=ql.QL_ACT_INT8_F16, a=FAKE[0], sc=FAKE[1], n_a=8, rows=None, off=FAKE[2], t=8, w=good, y=FAKE[6], ws=None,
+          ws_bytes=0):
         return L.qlinear_grouped_gemm(fmt, a, sc, n_a, rows, off, t, None if w is None else C.byref(ql.Experts(**w)), y,
-                                      None)
+                                      ws, ws_bytes, None)
 
     assert f(t=-1) == INVALID and f(n_a=-1) == INVALID and f(n_a=0) == INVALID and f(w=None) == INVALID
     for name in ("a", "sc", "off", "y"):
@@ -121,6 +122,12 @@ def test_experts_c_checks(ql):
     for fmt in (ql.QL_ROUTE_INT8, ql.QL_ROUTE_BF16, ql.QL_ROUTE_NVFP4, ql.QL_ACT_INT8_TENSOR, 99):
         assert f(fmt=fmt) == INVALID
     assert f(a=FAKE[0] + 2) == ALIGN and f(y=FAKE[6] + 2) == ALIGN
+    need = L.qlinear_grouped_gemm_ws_bytes(1000, C.byref(ql.Experts(**good)), 1)
+    assert need == 1000 * 128 * 2 and L.qlinear_grouped_gemm_ws_bytes(1000, C.byref(ql.Experts(**good)), 0) == 0
+    assert L.qlinear_grouped_gemm_ws_bytes(8, C.byref(ql.Experts(**good)), 1) == 0      # few rows: no copy
+    assert L.qlinear_grouped_gemm_ws_bytes(-1, C.byref(ql.Experts(**good)), 1) == 0
+    big = dict(t=1000, rows=FAKE[7])
+    assert f(**big) == 6 and f(**big, ws=FAKE[5], ws_bytes=need - 1) == 6 and f(**big, ws=FAKE[5] + 16, ws_bytes=need) == ALIGN
     assert f(off=FAKE[2] + 2) == ALIGN and f(rows=FAKE[7] + 2) == ALIGN and f(sc=FAKE[1] + 2) == ALIGN
 
 
