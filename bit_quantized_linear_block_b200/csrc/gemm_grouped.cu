@@ -99,6 +99,18 @@ __device__ __forceinline__ uint32_t grouped_idesc(int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
+// Whether the phase with the given parity has completed (no suspension).
+__device__ __forceinline__ bool mbar_test(uint32_t bar_addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar_addr), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
@@ -130,12 +142,38 @@ struct TileCursor {
   }
 };
 
-// Lane 0 waits for one or two mbarriers, the warp shares the outcome.
-__device__ __forceinline__ bool warp_wait_pair(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, long long limit,
-                                               volatile int* abort_flag) {
+// Position in a ring of N slots: the slot and the phase parity of its use.
+template <int N>
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Bounded wait of one thread; the abort flag is looked at only when the
+// phase is not complete yet.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, long long limit, volatile int* abort_flag) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const long long t0 = clock64();
+  while (*abort_flag == 0) {
+    if (mbar_try_wait(a, parity)) return true;
+    if (clock64() - t0 > limit) return false;
+  }
+  return false;
+}
+
+// The same for a warp: every lane looks, one lane waits if it has to, and
+// all take its outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long limit, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_test(smem_u32(bar), parity))) return true;
   int ok = 0;
-  if (lane_id() == 0)
-    ok = (*abort_flag == 0) && mbar_wait(a, pa, limit) && (b == nullptr || mbar_wait(b, pb, limit));
+  if (lane_id() == 0) ok = wait_or_abort(bar, parity, limit, abort_flag);
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
@@ -223,21 +261,22 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
     // ------------------------------------------------------------ weight producer
     if (elect_one()) {
       int it = 0;
+      RingPos<WS> w;
       bool ok = true;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         const GroupedTile g = cur.at(t, p.tiles_n, BMT);
         const uint8_t* sf = p.sf + static_cast<size_t>(g.e) * p.expert_sf + static_cast<size_t>(g.nb) * p.k_atoms * 512;
         const int wrow = g.e * p.N + g.nb * 128;
-        for (int c = 0; c < chunks; ++c, ++it) {
-          const int s = it % WS;
-          if (*abort_flag || !mbar_wait(&w_empty[s], ((it / WS) & 1) ^ 1, p.wait_limit)) {
+        for (int c = 0; c < chunks; ++c, ++it, w.advance()) {
+          if (!wait_or_abort(&w_empty[w.slot], w.phase ^ 1, p.wait_limit, abort_flag)) {
             ok = false;
             break;
           }
           const uint32_t sf_bytes = 512 * min(C::WK, p.num_kst - C::WK * c);
-          mbar_arrive_expect_tx(&w_full[s], C::W_BYTES + sf_bytes);
-          tma_load_2d(smem + C::OFF_W + s * C::W_BYTES, &tm_w, &w_full[s], c * (C::WK * C::BK / 2), wrow);
-          bulk_load(smem + C::OFF_SF + s * C::SF_BYTES, sf + static_cast<size_t>(c) * C::SF_BYTES, sf_bytes, &w_full[s]);
+          mbar_arrive_expect_tx(&w_full[w.slot], C::W_BYTES + sf_bytes);
+          tma_load_2d(smem + C::OFF_W + w.slot * C::W_BYTES, &tm_w, &w_full[w.slot], c * (C::WK * C::BK / 2), wrow);
+          bulk_load(smem + C::OFF_SF + w.slot * C::SF_BYTES, sf + static_cast<size_t>(c) * C::SF_BYTES, sf_bytes,
+                    &w_full[w.slot]);
         }
       }
       if (!ok) fail_timeout(p.status, abort_flag);
@@ -247,21 +286,22 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
     // ------------------------------------------------------------ activation producer
     if (elect_one()) {
       int it = 0;
+      RingPos<RS> b;
       bool ok = true;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         const GroupedTile g = cur.at(t, p.tiles_n, BMT);
         const int boxes = g.n > 128 ? 0 : (g.n + 63) >> 6;     // 0: one box of BMT rows
         const uint32_t bytes = g.n > 128 ? C::B_BYTES : 8192 * boxes;
-        for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
-          const int s = it % RS;
-          if (*abort_flag || !mbar_wait(&b_empty[s], ((it / RS) & 1) ^ 1, p.wait_limit)) {
+        for (int ks = 0; ks < p.num_kst; ++ks, ++it, b.advance()) {
+          if (!wait_or_abort(&b_empty[b.slot], b.phase ^ 1, p.wait_limit, abort_flag)) {
             ok = false;
             break;
           }
-          uint8_t* b = smem + C::OFF_B + s * C::B_BYTES;
-          mbar_arrive_expect_tx(&b_full[s], bytes);
-          if (boxes == 0) tma_load_2d(b, &tm_xw, &b_full[s], ks * C::BK, g.row0);
-          for (int i = 0; i < boxes; ++i) tma_load_2d(b + i * 8192, &tm_x, &b_full[s], ks * C::BK, g.row0 + 64 * i);
+          uint8_t* dst = smem + C::OFF_B + b.slot * C::B_BYTES;
+          uint64_t* full = &b_full[b.slot];
+          mbar_arrive_expect_tx(full, bytes);
+          if (boxes == 0) tma_load_2d(dst, &tm_xw, full, ks * C::BK, g.row0);
+          for (int i = 0; i < boxes; ++i) tma_load_2d(dst + i * 8192, &tm_x, full, ks * C::BK, g.row0 + 64 * i);
         }
       }
       if (!ok) fail_timeout(p.status, abort_flag);
@@ -270,35 +310,40 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
-      int it = 0, local = 0;
+      RingPos<RS> b;
+      RingPos<C::AS> a;
+      RingPos<C::NACC> d;
+      const uint64_t bdesc0 = smem_desc(smem_u32(smem + C::OFF_B), 0, 1024, kSwizzle128B);
       bool ok = true;
-      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, ++local) {
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, d.advance()) {
         const uint32_t idesc = grouped_idesc(cur.at(t, p.tiles_n, BMT).n);
-        const int acc = local % C::NACC;
-        if (*abort_flag || !mbar_wait(&tempty[acc], ((local / C::NACC) & 1) ^ 1, p.wait_limit)) {
+        if (!wait_or_abort(&tempty[d.slot], d.phase ^ 1, p.wait_limit, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem + acc * BMT;
-        for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
-          const int rs = it % RS, sl = it % C::AS;
-          if (*abort_flag || !mbar_wait(&b_full[rs], (it / RS) & 1, p.wait_limit) ||
-              !mbar_wait(&xf_full[sl], (it / C::AS) & 1, p.wait_limit)) {
+        const uint32_t d_tmem = tmem + d.slot * BMT;
+        uint32_t accumulate = 0;
+        for (int ks = 0; ks < p.num_kst; ++ks, b.advance(), a.advance()) {
+          if (!wait_or_abort(&b_full[b.slot], b.phase, p.wait_limit, abort_flag) ||
+              !wait_or_abort(&xf_full[a.slot], a.phase, p.wait_limit, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t b_base = smem_u32(smem + C::OFF_B + rs * C::B_BYTES);
+          // the descriptor's address field counts 16-byte units and has room for all of shared memory
+          const uint64_t bdesc = bdesc0 + static_cast<uint32_t>(b.slot * (C::B_BYTES >> 4));
+          const uint32_t a_tmem = a_slots + 32 * a.slot;
 #pragma unroll
-          for (int i = 0; i < C::BK / 16; ++i)
-            tc_mma_f16_ts(d_tmem, a_slots + 32 * sl + 8 * i, smem_desc(b_base + 32 * i, 0, 1024, kSwizzle128B), idesc,
-                          (ks > 0 || i > 0) ? 1u : 0u);
-          tc_commit(&b_empty[rs]);
-          tc_commit(&xf_empty[sl]);
+          for (int i = 0; i < C::BK / 16; ++i) {
+            tc_mma_f16_ts(d_tmem, a_tmem + 8 * i, bdesc + 2 * i, idesc, accumulate);
+            accumulate = 1;
+          }
+          tc_commit(&b_empty[b.slot]);
+          tc_commit(&xf_empty[a.slot]);
         }
         if (!ok) break;
-        tc_commit(&tfull[acc]);
+        tc_commit(&tfull[d.slot]);
       }
       if (!ok) fail_timeout(p.status, abort_flag);
       drain_mma(drain, p.status);
@@ -308,14 +353,15 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
     const uint32_t q = static_cast<uint32_t>(warp & 3);
     const uint32_t row = 32 * q + lane;
     const int group = (warp - 4) >> 2;
+    // this group's stages: A slot and weight chunk of each, by stage number
     int it0 = 0, chunk0 = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, it0 += p.num_kst, chunk0 += chunks) {
       for (int ks = (group + XG - it0 % XG) % XG; ks < p.num_kst; ks += XG) {
         const int it = it0 + ks, sl = it % C::AS;
         const int chunk = chunk0 + ks / C::WK, ws = chunk % WS, sub = ks % C::WK;
-        if (!warp_wait_pair(&w_full[ws], (chunk / WS) & 1, &xf_empty[sl], ((it / C::AS) & 1) ^ 1, p.wait_limit,
-                            abort_flag)) {
+        if (!warp_wait(&w_full[ws], (chunk / WS) & 1, p.wait_limit, abort_flag) ||
+            !warp_wait(&xf_empty[sl], ((it / C::AS) & 1) ^ 1, p.wait_limit, abort_flag)) {
           ok = false;
           break;
         }
