@@ -24,8 +24,8 @@
 //   warp 0      weight producer: 256-deep K chunks of the FP4 tile (128-byte
 //               rows, 128-byte swizzle) and their scales by TMA, WS-deep ring;
 //   warp 1      TMEM allocator and MMA issuer (kind::f16, A from tensor memory);
-//   warp 2      activation producer: 64-deep K stages, TMA boxes of 64 rows
-//               or one of BMT, RS-deep ring;
+//   warp 2      activation producer: 64-deep K stages, one TMA box of 64,
+//               128 or BMT rows, RS-deep ring;
 //   4 XG warps  transform: group g widens the stages with it % XG == g, lane
 //               l of lane quarter q its weight row 32 q + l, into one of AS
 //               32-column slots of tensor memory;
@@ -89,7 +89,7 @@ struct GroupedCfg {
   static constexpr int THREADS = (EPI0 + 8) * 32;
   static_assert(XG >= 1 && XG <= 3, "transform warp groups");
   static_assert(AS >= 2, "tensor memory budget");
-  static_assert(BMT % 64 == 0 && B_BYTES % 1024 == 0, "whole activation boxes");
+  static_assert(BMT >= 128 && B_BYTES % 1024 == 0, "whole activation boxes");
   static_assert(OFF_BAR % 8 == 0, "mbarrier alignment");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -179,9 +179,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long l
 
 template <int BMT, int RS, int WS, int XG>
 __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
-    k_gemm_grouped(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xw,
-                   const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_y,
-                   const GroupedArgs p) {
+    k_gemm_grouped(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x64,
+                   const __grid_constant__ CUtensorMap tm_x128, const __grid_constant__ CUtensorMap tm_w,
+                   const __grid_constant__ CUtensorMap tm_y, const GroupedArgs p) {
   using C = GroupedCfg<BMT, RS, WS, XG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
   const uint32_t lane = lane_id();
   if (threadIdx.x == 0) {
     prefetch_tmap(&tm_x);
-    prefetch_tmap(&tm_xw);
+    prefetch_tmap(&tm_x64);
+    prefetch_tmap(&tm_x128);
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_y);
     for (int i = 0; i < RS; ++i) {
@@ -290,18 +291,16 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
       bool ok = true;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         const GroupedTile g = cur.at(t, p.tiles_n, BMT);
-        const int boxes = g.n > 128 ? 0 : (g.n + 63) >> 6;     // 0: one box of BMT rows
-        const uint32_t bytes = g.n > 128 ? C::B_BYTES : 8192 * boxes;
+        // the smallest of the boxes of 64, 128 and BMT rows that covers the tile
+        const CUtensorMap* tm = g.n > 128 ? &tm_x : g.n > 64 ? &tm_x128 : &tm_x64;
+        const uint32_t bytes = 128 * (g.n > 128 ? BMT : g.n > 64 ? 128 : 64);
         for (int ks = 0; ks < p.num_kst; ++ks, ++it, b.advance()) {
           if (!wait_or_abort(&b_empty[b.slot], b.phase ^ 1, p.wait_limit, abort_flag)) {
             ok = false;
             break;
           }
-          uint8_t* dst = smem + C::OFF_B + b.slot * C::B_BYTES;
-          uint64_t* full = &b_full[b.slot];
-          mbar_arrive_expect_tx(full, bytes);
-          if (boxes == 0) tma_load_2d(dst, &tm_xw, full, ks * C::BK, g.row0);
-          for (int i = 0; i < boxes; ++i) tma_load_2d(dst + i * 8192, &tm_x, full, ks * C::BK, g.row0 + 64 * i);
+          mbar_arrive_expect_tx(&b_full[b.slot], bytes);
+          tma_load_2d(smem + C::OFF_B + b.slot * C::B_BYTES, tm, &b_full[b.slot], ks * C::BK, g.row0);
         }
       }
       if (!ok) fail_timeout(p.status, abort_flag);
@@ -473,11 +472,13 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
                                     int* status) {
   using C = GroupedCfg<BMT, RS, WS, XG>;
   const int N = w->N, K = w->K;
-  CUtensorMap tx, txw, tw, ty;
-  if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows != nullptr ? T : rows_a, static_cast<int64_t>(K) * 2, C::BK, 64,
-                    CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_tmap_2d(&txw, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, rows != nullptr ? T : rows_a, static_cast<int64_t>(K) * 2, C::BK, BMT,
-                    CU_TENSOR_MAP_SWIZZLE_128B) ||
+  const int64_t x_rows = rows != nullptr ? T : rows_a;
+  auto x_map = [&](CUtensorMap* map, int box_rows) {
+    return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, x_rows, static_cast<int64_t>(K) * 2, C::BK, box_rows,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  CUtensorMap tx, tx64, tx128, tw, ty;
+  if (!x_map(&tx, BMT) || !x_map(&tx64, 64) || !x_map(&tx128, 128) ||
       !make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, static_cast<int64_t>(w->E) * N, K / 2,
                     C::WK * C::BK / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, T, static_cast<int64_t>(N) * 2, 32, 32,
@@ -511,7 +512,7 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   auto kern = k_gemm_grouped<BMT, RS, WS, XG>;
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return QL_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(tiles, num_sms()));
-  if (launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, st, 1, tx, txw, tw, ty, p) != cudaSuccess) {
+  if (launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, st, 1, tx, tx64, tx128, tw, ty, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return QL_ERR_CUDA;
   }
