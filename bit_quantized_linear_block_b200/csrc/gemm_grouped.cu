@@ -67,29 +67,29 @@ struct GroupedArgs {
   int* status;
 };
 
-template <int BMT, int RS, int WS, int XG>
+template <int BMT, int RS, int WS>
 struct GroupedCfg {
-  static constexpr int BK = 64;                    // K elements of an activation stage
-  static constexpr int WK = 4;                     // stages of a weight chunk
-  static constexpr int NACC = (2 * BMT + 4 * 32 <= 512) ? 2 : 1;
-  static constexpr int AS = (512 - NACC * BMT) / 32 < 8 ? (512 - NACC * BMT) / 32 : 8;   // A slots
-  static constexpr int B_BYTES = BMT * BK * 2;
+  static constexpr int BK = 128;                   // K elements of a stage: two 64-element halves
+  static constexpr int WK = 2;                     // stages of a weight chunk
+  static constexpr int NACC = (2 * BMT + 2 * 64 <= 512) ? 2 : 1;
+  static constexpr int AS = (512 - NACC * BMT) / 64 < RS ? (512 - NACC * BMT) / 64 : RS;   // A slots of 64 columns
+  static constexpr int HALF_BYTES = BMT * 128;     // 64 f16 of K per row
+  static constexpr int B_BYTES = 2 * HALF_BYTES;
   static constexpr int W_BYTES = 128 * WK * BK / 2;
-  static constexpr int SF_BYTES = WK * 512;
+  static constexpr int SF_BYTES = WK * 1024;
   static constexpr int OFF_B = 0;
   static constexpr int OFF_W = OFF_B + RS * B_BYTES;
   static constexpr int OFF_SF = OFF_W + WS * W_BYTES;
   static constexpr int OFF_C = OFF_SF + WS * SF_BYTES;
   static constexpr int OFF_TAB = OFF_C + 8 * 2 * kWarpBoxBytes;      // first tile and first row of each expert
   static constexpr int OFF_BAR = OFF_TAB + 2 * 4 * (kMaxExperts + 4);
-  static constexpr int NBAR = 2 * RS + 2 * WS + 2 * AS + 2 * 2 + 1;
+  static constexpr int NBAR = 2 * RS + 2 * WS + AS + 2 * 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static constexpr int EPI0 = 4 + 4 * XG;
+  static constexpr int EPI0 = 12;
   static constexpr int THREADS = (EPI0 + 8) * 32;
-  static_assert(XG >= 1 && XG <= 3, "transform warp groups");
   static_assert(AS >= 2, "tensor memory budget");
-  static_assert(BMT >= 128 && B_BYTES % 1024 == 0, "whole activation boxes");
+  static_assert(BMT >= 128 && HALF_BYTES % 1024 == 0, "whole activation boxes");
   static_assert(OFF_BAR % 8 == 0, "mbarrier alignment");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -177,12 +177,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long l
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-template <int BMT, int RS, int WS, int XG>
-__global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
+template <int BMT, int RS, int WS>
+__global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
     k_gemm_grouped(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x64,
                    const __grid_constant__ CUtensorMap tm_x128, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_y, const GroupedArgs p) {
-  using C = GroupedCfg<BMT, RS, WS, XG>;
+  using C = GroupedCfg<BMT, RS, WS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
   uint64_t* b_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
   uint64_t* w_full = b_empty + RS;
   uint64_t* w_empty = w_full + WS;
   uint64_t* xf_full = w_empty + WS;
-  uint64_t* xf_empty = xf_full + C::AS;
-  uint64_t* tfull = xf_empty + C::AS;
+  uint64_t* tfull = xf_full + C::AS;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
@@ -213,12 +212,9 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
     }
     for (int i = 0; i < WS; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 4 * C::WK);       // four transform warps x the chunk's stages
+      mbar_init(&w_empty[i], 8 * C::WK);   // the transform warps x the chunk's stages
     }
-    for (int i = 0; i < C::AS; ++i) {
-      mbar_init(&xf_full[i], 4);
-      mbar_init(&xf_empty[i], 1);
-    }
+    for (int i = 0; i < C::AS; ++i) mbar_init(&xf_full[i], 8);   // the transform warps
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 8);
@@ -273,7 +269,7 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
             ok = false;
             break;
           }
-          const uint32_t sf_bytes = 512 * min(C::WK, p.num_kst - C::WK * c);
+          const uint32_t sf_bytes = 1024 * min(C::WK, p.num_kst - C::WK * c);
           mbar_arrive_expect_tx(&w_full[w.slot], C::W_BYTES + sf_bytes);
           tma_load_2d(smem + C::OFF_W + w.slot * C::W_BYTES, &tm_w, &w_full[w.slot], c * (C::WK * C::BK / 2), wrow);
           bulk_load(smem + C::OFF_SF + w.slot * C::SF_BYTES, sf + static_cast<size_t>(c) * C::SF_BYTES, sf_bytes,
@@ -293,14 +289,16 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
         const GroupedTile g = cur.at(t, p.tiles_n, BMT);
         // the smallest of the boxes of 64, 128 and BMT rows that covers the tile
         const CUtensorMap* tm = g.n > 128 ? &tm_x : g.n > 64 ? &tm_x128 : &tm_x64;
-        const uint32_t bytes = 128 * (g.n > 128 ? BMT : g.n > 64 ? 128 : 64);
+        const uint32_t bytes = 256 * (g.n > 128 ? BMT : g.n > 64 ? 128 : 64);
         for (int ks = 0; ks < p.num_kst; ++ks, ++it, b.advance()) {
           if (!wait_or_abort(&b_empty[b.slot], b.phase ^ 1, p.wait_limit, abort_flag)) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&b_full[b.slot], bytes);
-          tma_load_2d(smem + C::OFF_B + b.slot * C::B_BYTES, tm, &b_full[b.slot], ks * C::BK, g.row0);
+          uint8_t* dst = smem + C::OFF_B + b.slot * C::B_BYTES;
+          tma_load_2d(dst, tm, &b_full[b.slot], ks * C::BK, g.row0);
+          tma_load_2d(dst + C::HALF_BYTES, tm, &b_full[b.slot], ks * C::BK + 64, g.row0);
         }
       }
       if (!ok) fail_timeout(p.status, abort_flag);
@@ -332,14 +330,13 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
           tc_fence_after();
           // the descriptor's address field counts 16-byte units and has room for all of shared memory
           const uint64_t bdesc = bdesc0 + static_cast<uint32_t>(b.slot * (C::B_BYTES >> 4));
-          const uint32_t a_tmem = a_slots + 32 * a.slot;
+          const uint32_t a_tmem = a_slots + 64 * a.slot;
 #pragma unroll
           for (int i = 0; i < C::BK / 16; ++i) {
-            tc_mma_f16_ts(d_tmem, a_tmem + 8 * i, bdesc + 2 * i, idesc, accumulate);
+            tc_mma_f16_ts(d_tmem, a_tmem + 8 * i, bdesc + (i >> 2) * (C::HALF_BYTES >> 4) + 2 * (i & 3), idesc, accumulate);
             accumulate = 1;
           }
-          tc_commit(&b_empty[b.slot]);
-          tc_commit(&xf_empty[a.slot]);
+          tc_commit(&b_empty[b.slot]);   // frees the activation stage and the A slot
         }
         if (!ok) break;
         tc_commit(&tfull[d.slot]);
@@ -351,25 +348,24 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
     // ------------------------------------------------------------ transform
     const uint32_t q = static_cast<uint32_t>(warp & 3);
     const uint32_t row = 32 * q + lane;
-    const int group = (warp - 4) >> 2;
-    // this group's stages: A slot and weight chunk of each, by stage number
-    int it0 = 0, chunk0 = 0;
+    const int half = (warp - 4) >> 2;     // of the stage's K elements
+    int it = 0;
+    RingPos<C::AS> a;
+    RingPos<RS> freed;                    // the stage whose MMAs free the slot: it - AS
+    RingPos<WS> w;
     bool ok = true;
-    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, it0 += p.num_kst, chunk0 += chunks) {
-      for (int ks = (group + XG - it0 % XG) % XG; ks < p.num_kst; ks += XG) {
-        const int it = it0 + ks, sl = it % C::AS;
-        const int chunk = chunk0 + ks / C::WK, ws = chunk % WS, sub = ks % C::WK;
-        if (!warp_wait(&w_full[ws], (chunk / WS) & 1, p.wait_limit, abort_flag) ||
-            !warp_wait(&xf_empty[sl], ((it / C::AS) & 1) ^ 1, p.wait_limit, abort_flag)) {
+    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+      for (int ks = 0; ks < p.num_kst; ++ks, ++it) {
+        if (ks % C::WK == 0 && !warp_wait(&w_full[w.slot], w.phase, p.wait_limit, abort_flag)) {
           ok = false;
           break;
         }
-        tc_fence_after();
+        const int sub = 2 * (ks % C::WK) + half;   // 64-element piece of the weight chunk
         // scale atom: byte (row % 32) * 16 + (row / 32) * 4 + k16 holds the block scale of K block k16
-        const uint32_t sb4 = *reinterpret_cast<const uint32_t*>(smem + C::OFF_SF + ws * C::SF_BYTES + sub * 512 +
+        const uint32_t sb4 = *reinterpret_cast<const uint32_t*>(smem + C::OFF_SF + w.slot * C::SF_BYTES + sub * 512 +
                                                                 lane * 16 + q * 4);
         // 16-byte piece i of a swizzled 128-byte row sits at i ^ (row % 8)
-        const uint8_t* wr = smem + C::OFF_W + ws * C::W_BYTES + row * 128;
+        const uint8_t* wr = smem + C::OFF_W + w.slot * C::W_BYTES + row * 128;
         const uint4 c0 = *reinterpret_cast<const uint4*>(wr + (((2 * sub) ^ (row & 7)) << 4));
         const uint4 c1 = *reinterpret_cast<const uint4*>(wr + (((2 * sub + 1) ^ (row & 7)) << 4));
         const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
@@ -382,15 +378,26 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
           v[4 * w8 + 2] = o.z;
           v[4 * w8 + 3] = o.w;
         }
-        tmem_st32(a_slots + ((32 * q) << 16) + 32 * sl, v);
+        // the weights are widened in registers before the slot is waited for,
+        // so a slot's turn-around is only the store
+        if (it >= C::AS && !warp_wait(&b_empty[freed.slot], freed.phase, p.wait_limit, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st32(a_slots + ((32 * q) << 16) + 64 * a.slot + 32 * half, v);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
+        const bool last = ks % C::WK == C::WK - 1 || ks == p.num_kst - 1;   // of the chunk
         if (lane == 0) {
-          mbar_arrive(&xf_full[sl]);
-          // a chunk of two stages (the last one of some K) counts each twice
-          mbar_arrive_n(&w_empty[ws], p.num_kst - ks / C::WK * C::WK >= C::WK ? 1 : 2);
+          mbar_arrive(&xf_full[a.slot]);
+          // a chunk of one stage (the last one of some K) counts it twice
+          mbar_arrive_n(&w_empty[w.slot], last && ks % C::WK == 0 ? C::WK : 1);
         }
+        if (last) w.advance();
+        if (it >= C::AS) freed.advance();
+        a.advance();
         __syncwarp();   // the tcgen05 instructions need the whole warp together
       }
     }
@@ -466,15 +473,15 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, XG>::THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int BMT, int RS, int WS, int XG>
+template <int BMT, int RS, int WS>
 static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                                     const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
                                     int* status) {
-  using C = GroupedCfg<BMT, RS, WS, XG>;
+  using C = GroupedCfg<BMT, RS, WS>;
   const int N = w->N, K = w->K;
   const int64_t x_rows = rows != nullptr ? T : rows_a;
   auto x_map = [&](CUtensorMap* map, int box_rows) {
-    return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, x_rows, static_cast<int64_t>(K) * 2, C::BK, box_rows,
+    return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, x_rows, static_cast<int64_t>(K) * 2, 64, box_rows,
                         CU_TENSOR_MAP_SWIZZLE_128B);
   };
   CUtensorMap tx, tx64, tx128, tw, ty;
@@ -509,7 +516,7 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   const int64_t e = std::min<int64_t>(w->E, T);
   const int64_t tiles = (e + (T - e) / BMT) * p.tiles_n;
   if (tiles > 0x7FFFFFFF - num_sms()) return QL_ERR_UNSUPPORTED_SHAPE;
-  auto kern = k_gemm_grouped<BMT, RS, WS, XG>;
+  auto kern = k_gemm_grouped<BMT, RS, WS>;
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return QL_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(tiles, num_sms()));
   if (launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, st, 1, tx, tx64, tx128, tw, ty, p) != cudaSuccess) {
@@ -556,7 +563,7 @@ ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows
     }
     x = gathered;
   }
-  return launch_grouped_cfg<192, 6, 2, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+  return launch_grouped_cfg<192, 3, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
 }
 
 }  // namespace ql
