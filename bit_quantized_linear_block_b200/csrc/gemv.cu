@@ -32,6 +32,8 @@
 // significant bits against the 8 of the bf16 output, and exact for an
 // unrotated block's bf16 values down to 2^-29 of its largest; the block's
 // sums are scaled back in fp32.
+#include <type_traits>
+
 #include "ql_common.cuh"
 #include "gemm_common.cuh"
 #include "launchers.h"
@@ -93,6 +95,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ uint32_t h2_bits(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
 
+// As mma_f16 with a zero accumulator.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Eight E2M1 codes -> four f16x2 words of their values (hardware convert).
 __device__ __forceinline__ void fp4x8_to_f16(uint32_t codes, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
@@ -104,6 +116,14 @@ __device__ __forceinline__ void fp4x8_to_f16(uint32_t codes, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(codes));
 }
+// The two E4M3 scales in the low half of `v`.
+__device__ __forceinline__ __half2 e4m3x2_to_f16(uint32_t v) {
+  uint32_t s;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(v)));
+  return bits_h2(s);
+}
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t v) { return __half22float2(e4m3x2_to_f16(v)); }
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // int8 x4 -> two f16x2 words of the exact values (a byte permute builds
 // 1024 + (q + 128) in f16, a packed subtract removes the offset).
@@ -201,8 +221,9 @@ __device__ __forceinline__ float block_to_f16(const uint4 (&raw)[4], int hadamar
 
 }  // namespace
 
-// NT: tiles of 8 rows of `a` (1: up to 8 rows, 2: up to 16).
-template <int NT, int ACT, bool GROUPED>
+// NT: tiles of 8 rows of `a` (1: up to 8 rows, 2: up to 16).  ONE: the form
+// for a single row (0 never, 1 always, 2 where a row tile has one row).
+template <int NT, int ACT, bool GROUPED, int ONE>
 __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(const GvArgs p) {
   constexpr int kTokens = 8 * NT;
   constexpr bool kScaled = ACT == kGvBf16;       // a factor per row and K block
@@ -286,6 +307,7 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
 
   // Rows of `a`: lane group g (four lanes) converts one (block, row) pair of a
   // batch of `gb` blocks x `m2` rows, gb m2 = 8 (NT = 2: one block, 8 rows twice).
+  const bool one = NT == 1 && (ONE == 1 || (ONE == 2 && M == 1));
   const int m2 = NT == 2 ? 8 : M > 4 ? 8 : M > 2 ? 4 : M;
   const int gb = 8 / m2;
   const int pair_blk = g / m2, pair_row = g - pair_blk * m2;
@@ -340,67 +362,100 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
       const int j = j0 + b;
       cp_async_wait<kGvDepth - 1>();             // this lane's own pieces of block j have landed
       const uint8_t* slot = ring + (j % kGvDepth) * kGvStage + 16 * lane;
-      uint4 xf[NT][4];                           // B fragments: row g of the tile, elements 32 t + 8 q ..
+      // B fragments: row g of the tile, elements 32 t + 8 q ..; for a single
+      // row, column g takes scale block g's elements only
+      uint4 xf[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          xf[nt][q] = g < m2 ? lds128(xbuf + nt * 2048 + q * 512 + (b * m2 * 4 + lane) * 16)
-                             : make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < 4; ++q) {
+          const bool mine = one ? g == 2 * t + (q >> 1) : g < m2;
+          xf[nt][q] = mine ? lds128(xbuf + nt * 2048 + q * 512 + (one ? 4 * b + t : b * m2 * 4 + lane) * 16)
+                           : make_uint4(0, 0, 0, 0);
+        }
       const uint4 sa = lds128(slot + kGvCodeBytes), sb = lds128(slot + kGvCodeBytes + 512);
       const uint32_t sa4[4] = {sa.x, sa.y, sa.z, sa.w}, sb4[4] = {sb.x, sb.y, sb.z, sb.w};
       float f0[NT], f1[NT];
       if constexpr (kScaled) {                   // factors of rows 2t and 2t + 1 (columns of the accumulator)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          f0[nt] = xscale[8 * nt + min(b * m2 + 2 * t, 7)];
+          f0[nt] = xscale[8 * nt + (one ? b : min(b * m2 + 2 * t, 7))];
           f1[nt] = xscale[8 * nt + min(b * m2 + 2 * t + 1, 7)];
         }
       }
+      // All four tiles, step by step, so that their chains of dependent MMAs
+      // overlap (tile by tile a block took about XX% longer).  A tile past N
+      // multiplies what its ring slot happens to hold; nothing of it is stored.
+      uint4 ca[4], cb[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (i >= ntiles) break;                  // warp-uniform
-        const uint4 ca = lds128(slot + (2 * i) * 512), cb = lds128(slot + (2 * i + 1) * 512);
-        const uint32_t ca4[4] = {ca.x, ca.y, ca.z, ca.w}, cb4[4] = {cb.x, cb.y, cb.z, cb.w};
-        // the two block scales of elements 32 t .. 32 t + 31, as f16 pairs
-        uint32_t s2a, s2b;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2a) : "h"(static_cast<uint16_t>(sa4[i] >> (16 * (t & 1)))));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2b) : "h"(static_cast<uint16_t>(sb4[i] >> (16 * (t & 1)))));
-        const __half2 va[2] = {__low2half2(bits_h2(s2a)), __high2half2(bits_h2(s2a))};
-        const __half2 vb[2] = {__low2half2(bits_h2(s2b)), __high2half2(bits_h2(s2b))};
-        float part[NT][4];
-        if constexpr (kScaled) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) part[nt][c] = 0.f;
-        }
+        ca[i] = lds128(slot + (2 * i) * 512);
+        cb[i] = lds128(slot + (2 * i + 1) * 512);
+      }
+      if (one) {
+        // Column c of the accumulator is the sum over scale block c of the
+        // unscaled values, so each lane scales its columns 2 t and 2 t + 1 in
+        // fp32, four values a tile, instead of 32 f16 pairs of weights.
+        float part[4][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t ha[4], hb[4];
+            fp4x8_to_f16(word_of(ca[i], q), ha);
+            fp4x8_to_f16(word_of(cb[i], q), hb);
+            if (q == 0) mma_f16_zero(part[i], ha[0], hb[0], ha[1], hb[1], xf[0][q].x, xf[0][q].y);
+            else mma_f16(part[i], ha[0], hb[0], ha[1], hb[1], xf[0][q].x, xf[0][q].y);
+            mma_f16(part[i], ha[2], hb[2], ha[3], hb[3], xf[0][q].z, xf[0][q].w);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 fa = e4m3x2_to_f32(sa4[i] >> (16 * (t & 1))), fb = e4m3x2_to_f32(sb4[i] >> (16 * (t & 1)));
+          const float va = fmaf(part[i][1], fa.y, __fmul_rn(part[i][0], fa.x));
+          const float vb = fmaf(part[i][3], fb.y, __fmul_rn(part[i][2], fb.x));
+          acc[i][0][0] = kScaled ? fmaf(va, f0[0], acc[i][0][0]) : acc[i][0][0] + va;
+          acc[i][0][2] = kScaled ? fmaf(vb, f0[0], acc[i][0][2]) : acc[i][0][2] + vb;
+        }
+        issue(j + kGvDepth);
+        continue;
+      }
+      float part[4][NT][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // scales of elements 32 t .. 32 t + 31, one per 16; this q's as an f16 pair
+          const __half2 s2a = e4m3x2_to_f16(sa4[i] >> (16 * (t & 1))), s2b = e4m3x2_to_f16(sb4[i] >> (16 * (t & 1)));
+          const __half2 va = q < 2 ? __low2half2(s2a) : __high2half2(s2a);
+          const __half2 vb = q < 2 ? __low2half2(s2b) : __high2half2(s2b);
           uint32_t ha[4], hb[4];
-          fp4x8_to_f16(ca4[q], ha);
-          fp4x8_to_f16(cb4[q], hb);
+          fp4x8_to_f16(word_of(ca[i], q), ha);
+          fp4x8_to_f16(word_of(cb[i], q), hb);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            ha[c] = h2_bits(__hmul2(bits_h2(ha[c]), va[q >> 1]));
-            hb[c] = h2_bits(__hmul2(bits_h2(hb[c]), vb[q >> 1]));
+            ha[c] = h2_bits(__hmul2(bits_h2(ha[c]), va));
+            hb[c] = h2_bits(__hmul2(bits_h2(hb[c]), vb));
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float (&d)[4] = kScaled ? part[nt] : acc[i][nt];
-            mma_f16(d, ha[0], hb[0], ha[1], hb[1], xf[nt][q].x, xf[nt][q].y);
+            float (&d)[4] = kScaled ? part[i][nt] : acc[i][nt];
+            if (kScaled && q == 0) mma_f16_zero(d, ha[0], hb[0], ha[1], hb[1], xf[nt][q].x, xf[nt][q].y);
+            else mma_f16(d, ha[0], hb[0], ha[1], hb[1], xf[nt][q].x, xf[nt][q].y);
             mma_f16(d, ha[2], hb[2], ha[3], hb[3], xf[nt][q].z, xf[nt][q].w);
           }
         }
-        if constexpr (kScaled) {
+      }
+      if constexpr (kScaled) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            acc[i][nt][0] = fmaf(part[nt][0], f0[nt], acc[i][nt][0]);
-            acc[i][nt][1] = fmaf(part[nt][1], f1[nt], acc[i][nt][1]);
-            acc[i][nt][2] = fmaf(part[nt][2], f0[nt], acc[i][nt][2]);
-            acc[i][nt][3] = fmaf(part[nt][3], f1[nt], acc[i][nt][3]);
+            acc[i][nt][0] = fmaf(part[i][nt][0], f0[nt], acc[i][nt][0]);
+            acc[i][nt][1] = fmaf(part[i][nt][1], f1[nt], acc[i][nt][1]);
+            acc[i][nt][2] = fmaf(part[i][nt][2], f0[nt], acc[i][nt][2]);
+            acc[i][nt][3] = fmaf(part[i][nt][3], f1[nt], acc[i][nt][3]);
           }
-        }
       }
       issue(j + kGvDepth);                       // the slot just read
     }
@@ -412,6 +467,15 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
   constexpr int kPitch = kGvRows + 1;
   float* red = reinterpret_cast<float*>(smem);   // [warps][kTokens][kPitch], then [kTokens][kPitch] sums
   float* sum = red + warps * kTokens * kPitch;
+  if (one) {   // a row's sum is spread over the four lanes of its scale blocks
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        acc[i][0][c] += __shfl_xor_sync(0xffffffffu, acc[i][0][c], 1);
+        acc[i][0][c] += __shfl_xor_sync(0xffffffffu, acc[i][0][c], 2);
+      }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -465,7 +529,7 @@ int gemv_units(int32_t N) {
 }
 
 // tiles: row tiles (grouped: the most that the experts' rows can make).
-template <int NT, int ACT, bool GROUPED>
+template <int NT, int ACT, bool GROUPED, int ONE>
 ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   const int units = gemv_units(p.N), kb = p.K / 128;
   // enough CTAs for two on every SM, as far as K gives each warp a block
@@ -481,7 +545,7 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   const int ring = warps * (kGvDepth * kGvStage + NT * 2048 + NT * 32);
   const int red = (warps + 1) * 8 * NT * (kGvRows + 1) * 4;
   const int smem = std::max(ring, red);
-  auto kern = k_gemv<NT, ACT, GROUPED>;
+  auto kern = k_gemv<NT, ACT, GROUPED, ONE>;
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), smem)) return QL_ERR_CUDA;
   if (launch_pdl(kern, dim3(static_cast<unsigned>(ctas * S)), dim3(32 * warps), smem, st, S, p) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -508,13 +572,16 @@ ql_status launch_gemv(int act, const void* a, const float* a_scales, int64_t M, 
   p.K = w->K;
   p.hadamard = w->hadamard;
   p.alpha_mul = w->hadamard ? (1.0f / 128.0f) : 1.0f;
-  if (M <= 8)
-    return act == 0 ? launch_gemv_cfg<1, kGvBf16, false>(p, 1, st)
-           : act == 1 ? launch_gemv_cfg<1, kGvF16, false>(p, 1, st)
-                      : launch_gemv_cfg<1, kGvI8, false>(p, 1, st);
-  return act == 0 ? launch_gemv_cfg<2, kGvBf16, false>(p, 1, st)
-         : act == 1 ? launch_gemv_cfg<2, kGvF16, false>(p, 1, st)
-                    : launch_gemv_cfg<2, kGvI8, false>(p, 1, st);
+  auto by_act = [&](auto nt, auto one) {
+    constexpr int NT = decltype(nt)::value, ONE = decltype(one)::value;
+    return act == 0   ? launch_gemv_cfg<NT, kGvBf16, false, ONE>(p, 1, st)
+           : act == 1 ? launch_gemv_cfg<NT, kGvF16, false, ONE>(p, 1, st)
+                      : launch_gemv_cfg<NT, kGvI8, false, ONE>(p, 1, st);
+  };
+  using std::integral_constant;
+  if (M == 1) return by_act(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  if (M <= 8) return by_act(integral_constant<int, 1>{}, integral_constant<int, 0>{});
+  return by_act(integral_constant<int, 2>{}, integral_constant<int, 0>{});
 }
 
 ql_status launch_grouped_few(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
@@ -540,7 +607,7 @@ ql_status launch_grouped_few(const void* a, const float* a_scales, int64_t rows_
     const int64_t e = std::min<int64_t>(w->E, T);
     return e + (T - e) / per;
   };
-  return T <= 8 ? launch_gemv_cfg<1, kGvF16, true>(p, tiles(8), st) : launch_gemv_cfg<2, kGvF16, true>(p, tiles(16), st);
+  return T <= 8 ? launch_gemv_cfg<1, kGvF16, true, 2>(p, tiles(8), st) : launch_gemv_cfg<2, kGvF16, true, 0>(p, tiles(16), st);
 }
 
 }  // namespace ql

@@ -135,10 +135,17 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+# The handle of a device's current stream without making a Stream object
+# (0.1 against 2.2 us of a call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device):
     """The stream handle to launch on: the given one (which must belong to
     `device`) or the current stream of `device`."""
     if stream is None:
+        if _raw_stream is not None and device.index is not None:
+            return C.c_void_p(_raw_stream(device.index))
         return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the call runs on {device}")

@@ -86,14 +86,18 @@ def test_agrees_with_the_tiled_product(ql, m):
 
 
 def test_rows_do_not_depend_on_their_company(ql):
-    """A row alone, among others, beside a row of NaN, infinity or huge values,
-    and repeated: the same bits (the row's products and sums are its own)."""
-    w, _ = _layer(ql, 384, 1920, 5)
+    """A row among up to 7 or 15 others, beside a row of NaN, infinity or huge
+    values, and repeated: the same bits (the row's products and sums are its
+    own).  A single row's sums run in another order: within the bound."""
+    w, wq = _layer(ql, 384, 1920, 5)
     x = S.activations_fixed_outliers(8, 1920, 8, 50.0, 9, 1).cuda()
     y = ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x), 8, w)
     assert torch.equal(y, ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x), 8, w))
     for i in range(8):
-        assert torch.equal(y[i:i + 1], ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x[i:i + 1].contiguous()), 1, w))
+        one = ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x[i:i + 1].contiguous()), 1, w)
+        _check(ql, x[i:i + 1], None, ql.QL_ROUTE_BF16, wq, True, one)
+        two = ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x[[i, (i + 1) % 8]].contiguous()), 2, w)
+        assert torch.equal(two, y[[i, (i + 1) % 8]])
     both = torch.cat((x, x))
     assert torch.equal(ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=both), 16, w), torch.cat((y, y)))
     bad = x.clone()
