@@ -32,7 +32,9 @@
 // significant bits against the 8 of the bf16 output, and exact for an
 // unrotated block's bf16 values down to 2^-29 of its largest; the block's
 // sums are scaled back in fp32.
+#include <mutex>
 #include <type_traits>
+#include <unordered_map>
 
 #include "ql_common.cuh"
 #include "gemm_common.cuh"
@@ -77,11 +79,12 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+// The two halves of cluster_sync().
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // D (16 x 8, fp32) += A (16 x 16, f16) B (16 x 8, f16)
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -462,11 +465,12 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
   }
   cp_async_wait<0>();
   __syncthreads();                               // the ring is free: it becomes the reduction buffer
+  if (S > 1) cluster_arrive();
 
   // acc[i][nt][c]: weight row 16 i + g + 8 (c / 2) of the unit, row 8 nt + 2 t + c % 2 of a
   constexpr int kPitch = kGvRows + 1;
-  float* red = reinterpret_cast<float*>(smem);   // [warps][kTokens][kPitch], then [kTokens][kPitch] sums
-  float* sum = red + warps * kTokens * kPitch;
+  float* red = reinterpret_cast<float*>(smem);   // [warps][kTokens][kPitch]
+  float* parts = red + warps * kTokens * kPitch; // the cluster's first CTA: [S][kTokens][kGvRows]
   if (one) {   // a row's sum is spread over the four lanes of its scale blocks
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -484,27 +488,31 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
       for (int c = 0; c < 4; ++c)
         red[(warp * kTokens + 8 * nt + 2 * t + (c & 1)) * kPitch + 16 * i + g + 8 * (c >> 1)] = acc[i][nt][c];
   __syncthreads();
-  for (int o = threadIdx.x; o < M * kGvRows; o += blockDim.x) {
-    const int m = o >> 6, r = o & 63;
+  auto warps_sum = [&](int m, int r) {
     float v = 0.f;
     for (int w = 0; w < warps; ++w) v += red[(w * kTokens + m) * kPitch + r];
-    sum[m * kPitch + r] = v;
+    return v;
+  };
+  if (S > 1) {   // the CTA's sums to the cluster's first CTA
+    cluster_wait();   // every CTA of the cluster has started, and the first one's ring is free
+    const uint32_t dst = map_to_rank(smem_u32(parts + rank * kTokens * kGvRows), 0);
+    for (int o = threadIdx.x; o < M * kGvRows; o += blockDim.x) st_cluster_f32(dst + 4 * o, warps_sum(o >> 6, o & 63));
+    __syncwarp();
+    cluster_sync();
+    if (rank != 0) {
+      pdl_release();
+      return;
+    }
   }
-  __syncwarp();
-  if (S > 1) cluster_sync();
-  else __syncthreads();
   const float alpha = __fmul_rn(ld_dep(gscale), p.alpha_mul);
-  // the cluster's CTAs share the unit's outputs
-  for (int o = rank * blockDim.x + threadIdx.x; o < M * kGvRows; o += S * blockDim.x) {
+  for (int o = threadIdx.x; o < M * kGvRows; o += blockDim.x) {
     const int m = o >> 6, r = o & 63;
     const int n = first + 32 * (r >> 4) + (r & 15);
     float v = 0.f;
-    if (S > 1) {
-      const uint32_t addr = smem_u32(sum + m * kPitch + r);
-      for (int c = 0; c < S; ++c) v += ld_cluster_f32(map_to_rank(addr, c));
-    } else {
-      v = sum[m * kPitch + r];
-    }
+    if (S > 1)
+      for (int c = 0; c < S; ++c) v += parts[c * kTokens * kGvRows + o];
+    else
+      v = warps_sum(m, r);
     if (n < p.N) {
       float a = alpha;
       if constexpr (ACT != kGvBf16) {
@@ -516,8 +524,6 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
     }
   }
   pdl_release();
-  __syncwarp();
-  if (S > 1) cluster_sync();                     // no CTA leaves while another reads its sums
 }
 
 namespace {
@@ -528,24 +534,68 @@ int gemv_units(int32_t N) {
   return 2 * (N / 128) + (r == 0 ? 0 : r > 16 ? 2 : 1);
 }
 
+// Warps of this kernel that an SM's registers hold.
+int gemv_warps_per_sm(const void* kern) {
+  static std::mutex mu;
+  static std::unordered_map<const void*, int> known;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto it = known.find(kern);
+  if (it != known.end()) return it->second;
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 8;
+  }
+  return known[kern] = 65536 / (32 * ((a.numRegs + 7) / 8 * 8));
+}
+
 // tiles: row tiles (grouped: the most that the experts' rows can make).
 template <int NT, int ACT, bool GROUPED, int ONE>
 ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   const int units = gemv_units(p.N), kb = p.K / 128;
-  // enough CTAs for two on every SM, as far as K gives each warp a block
   const int64_t ctas = units * tiles;
-  int S = static_cast<int>(std::min<int64_t>(kGvMaxCluster, std::max<int64_t>(1, 2 * num_sms() / ctas)));
-  S = std::min(S, (kb + 1) / 2);
-  if (S < 1) S = 1;
-  const int per_cta = (kb + S - 1) / S;
-  const int warps = std::min(kGvMaxWarps, per_cta);
+  auto kern = k_gemv<NT, ACT, GROUPED, ONE>;
+  auto smem_for = [&](int warps, int S) {
+    const int ring = warps * (kGvDepth * kGvStage + NT * 2048 + NT * 32);
+    const int red = 8 * NT * (warps * (kGvRows + 1) + (S > 1 ? S * kGvRows : 0)) * 4;
+    return std::max(ring, red);
+  };
+  // Warps of a CTA: one K block each (four at least: they all add up the
+  // partial sums), as far as two CTAs (one, if that is all an SM gets) stay
+  // resident together: 16 rows x 15360 x 5120 took 19.5 us in one wave of 6
+  // warps a CTA and 24.2 in two of 8.
+  const int reg_warps = gemv_warps_per_sm(reinterpret_cast<const void*>(kern));
+  auto sm_ctas = [&](int S) { return (ctas * S + num_sms() - 1) / num_sms(); };   // of the fullest SM
+  auto warps_for = [&](int S) {
+    const int64_t together = std::min<int64_t>(sm_ctas(S), 2);
+    int warps = std::max(4, std::min(kGvMaxWarps, (kb + S - 1) / S));
+    while (warps > 4 && (together * warps > reg_warps || together * (smem_for(warps, S) + 1024) > 227 * 1024)) --warps;
+    return warps;
+  };
+  // K split over S CTAs, all of them resident at once (clusters that had to
+  // wait for room were slow: 5120 x 13824 12.5 us at S = 3, 20 at 7): the
+  // least of 115 ns per K block of the fullest SM, 200 ns per block that a
+  // warp takes in turn and 500 ns for a cluster's barrier and hand-over,
+  // which fits the times of one int8 row within 10%: 1920 x 1920 4.1 us at
+  // S = 4 and 5.3 at 1, 7680 x 1920 5.4 at 1 and 5.6 at 4, 15360 x 5120 12.5
+  // at 1 and 13.1 at 2.
+  int S = 1;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= kGvMaxCluster && (s == 1 || 2 * s <= kb); ++s) {
+    const int64_t per_cta = (kb + s - 1) / s, warps = warps_for(s);
+    if (s > 1 && sm_ctas(s) * warps > reg_warps) break;
+    const int64_t cost =
+        115 * sm_ctas(s) * per_cta + 200 * ((per_cta + warps - 1) / warps) + (s > 1 ? 500 : 0);
+    if (cost < best) {
+      best = cost;
+      S = s;
+    }
+  }
+  const int warps = warps_for(S);
   if (ctas * S > 0x7FFFFFFF) return QL_ERR_UNSUPPORTED_SHAPE;
   p.cluster = S;
   p.units = units;
-  const int ring = warps * (kGvDepth * kGvStage + NT * 2048 + NT * 32);
-  const int red = (warps + 1) * 8 * NT * (kGvRows + 1) * 4;
-  const int smem = std::max(ring, red);
-  auto kern = k_gemv<NT, ACT, GROUPED, ONE>;
+  const int smem = smem_for(warps, S);
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), smem)) return QL_ERR_CUDA;
   if (launch_pdl(kern, dim3(static_cast<unsigned>(ctas * S)), dim3(32 * warps), smem, st, S, p) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -607,7 +657,9 @@ ql_status launch_grouped_few(const void* a, const float* a_scales, int64_t rows_
     const int64_t e = std::min<int64_t>(w->E, T);
     return e + (T - e) / per;
   };
-  return T <= 8 ? launch_gemv_cfg<1, kGvF16, true, 2>(p, tiles(8), st) : launch_gemv_cfg<2, kGvF16, true, 0>(p, tiles(16), st);
+  // tiles of 8 rows unless the experts' rows fill more on average
+  return T <= 8 * static_cast<int64_t>(w->E) ? launch_gemv_cfg<1, kGvF16, true, 2>(p, tiles(8), st)
+                                             : launch_gemv_cfg<2, kGvF16, true, 0>(p, tiles(16), st);
 }
 
 }  // namespace ql
