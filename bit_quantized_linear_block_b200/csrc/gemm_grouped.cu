@@ -20,26 +20,42 @@
 // A tile costs what its rows need: the MMA's N, the loaded boxes and the
 // stored boxes follow its height.
 //
-// Persistent, one CTA per SM, warps by role:
+// Persistent, one CTA per SM, warps by role (K in pieces of 64; a stage is H
+// pieces, H = 2, or 4 for low tiles):
 //   warp 0      weight producer: 256-deep K chunks of the FP4 tile (128-byte
 //               rows, 128-byte swizzle) and their scales by TMA, WS-deep ring;
 //   warp 1      TMEM allocator and MMA issuer (kind::f16, A from tensor memory);
-//   warp 2      activation producer: 64-deep K stages, one TMA box of 64,
-//               128 or BMT rows, RS-deep ring;
-//   4 XG warps  transform: group g widens the stages with it % XG == g, lane
-//               l of lane quarter q its weight row 32 q + l, into one of AS
-//               32-column slots of tensor memory;
+//   warp 2      activation producer: a stage is one TMA box of rows per piece,
+//               of the smallest of three heights that covers the tile, RS-deep
+//               ring;
+//   4 H warps   transform: four warps widen piece h of every stage, lane l of
+//               lane quarter q its weight row 32 q + l, in registers first and
+//               then, once the MMAs of stage it - AS are done, into one of AS
+//               tensor-memory slots;
 //   8 warps     epilogue: a TMEM lane quarter each, every other 32-row box:
 //               scale, bf16, and a TMA store of the 32 x 32 box through the
 //               warp's own staging buffer.  A box that reaches past its
 //               segment is stored row by row, so no row of another segment
 //               or behind the last one is written.
-// Issue is what bounds the producers: a TMA instruction costs its thread
-// about a hundred cycles here, and each box row is a request.  So one lane
-// picked by elect.sync issues (behind `lane == 0` an instruction took about
-// 200 cycles more: 711 against 497 us at five per stage, 17664 x 7680 x
-// 1920), the weights come four stages at a time, and weights and activations
-// have a warp each.
+//
+// What bounds a stage, and what that led to (17664 x 7680 x 1920 and, where
+// weights dominate, 32 experts x 192 rows x 1920 x 7680; B200):
+//   * the producers' issue: a TMA instruction costs its thread a hundred
+//     cycles or two.  One lane picked by elect.sync issues (behind `lane == 0`
+//     711 against 497 us at five per 64-deep stage), the weights come 256
+//     deep, and weights and activations have a warp each: 388 us;
+//   * the MMA thread: about 130 cycles for each barrier that it passes and
+//     170 for its MMAs and commits, 450 a stage whatever the tile's height.
+//     Ring positions instead of divisions, the abort flag only behind a
+//     failed wait: 365 us; stages of two or four pieces with one commit for
+//     activations and A slot, see the next;
+//   * the slot's turn-around: MMA, commit, wait, widening, store.  Widening
+//     before the wait leaves only the store in it: 343 us, 1519 TFLOP/s
+//     (0.88 of the measured bf16 peak), and 144 us (165 before).
+// With few rows per expert the transform warps' instructions bound it
+// (conversions, f16x2 products and byte permutes all run at 64 lanes a cycle
+// and SM): 32 experts of 32 rows x 1920 x 7680 take 79 us against 41 for the
+// weights' bytes.
 // All waits are bounded; on a timeout a role records it, drains its own
 // copies or MMAs and leaves the loop, and the CTA frees its tensor memory.
 #include "ql_common.cuh"
@@ -67,16 +83,20 @@ struct GroupedArgs {
   int* status;
 };
 
-template <int BMT, int RS, int WS>
+template <int BMT, int RS, int WS, int H>
 struct GroupedCfg {
-  static constexpr int BK = 128;                   // K elements of a stage: two 64-element halves
-  static constexpr int WK = 2;                     // stages of a weight chunk
-  static constexpr int NACC = (2 * BMT + 2 * 64 <= 512) ? 2 : 1;
-  static constexpr int AS = (512 - NACC * BMT) / 64 < RS ? (512 - NACC * BMT) / 64 : RS;   // A slots of 64 columns
-  static constexpr int HALF_BYTES = BMT * 128;     // 64 f16 of K per row
-  static constexpr int B_BYTES = 2 * HALF_BYTES;
-  static constexpr int W_BYTES = 128 * WK * BK / 2;
-  static constexpr int SF_BYTES = WK * 1024;
+  static constexpr int BK = 64 * H;                // K elements of a stage: H pieces of 64
+  static constexpr int WK = 4 / H;                 // stages of a weight chunk (256 elements)
+  static constexpr int NACC = 2;
+  static constexpr int ACOLS = 32 * H;             // tensor-memory columns of an A slot
+  static constexpr int FREE = (512 - NACC * BMT) / ACOLS;
+  static constexpr int AS = FREE < RS ? FREE : RS; // A slots
+  static constexpr int BOX1 = BMT == 192 ? 128 : BMT / 2;   // smaller activation boxes
+  static constexpr int BOX2 = BMT == 192 ? 64 : BMT / 4;
+  static constexpr int PIECE_BYTES = BMT * 128;    // 64 f16 of K per row
+  static constexpr int B_BYTES = H * PIECE_BYTES;
+  static constexpr int W_BYTES = 128 * 128;
+  static constexpr int SF_BYTES = 4 * 512;
   static constexpr int OFF_B = 0;
   static constexpr int OFF_W = OFF_B + RS * B_BYTES;
   static constexpr int OFF_SF = OFF_W + WS * W_BYTES;
@@ -86,10 +106,11 @@ struct GroupedCfg {
   static constexpr int NBAR = 2 * RS + 2 * WS + AS + 2 * 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static constexpr int EPI0 = 12;
+  static constexpr int EPI0 = 4 + 4 * H;           // first epilogue warp
   static constexpr int THREADS = (EPI0 + 8) * 32;
   static_assert(AS >= 2, "tensor memory budget");
-  static_assert(BMT >= 128 && HALF_BYTES % 1024 == 0, "whole activation boxes");
+  static_assert(H == 2 || H == 4, "a weight chunk is two stages or one");
+  static_assert(PIECE_BYTES % 1024 == 0 && BOX2 % 8 == 0, "whole swizzle atoms");
   static_assert(OFF_BAR % 8 == 0, "mbarrier alignment");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -177,12 +198,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long l
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-template <int BMT, int RS, int WS>
-__global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
-    k_gemm_grouped(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x64,
-                   const __grid_constant__ CUtensorMap tm_x128, const __grid_constant__ CUtensorMap tm_w,
+template <int BMT, int RS, int WS, int H>
+__global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, H>::THREADS, 1)
+    k_gemm_grouped(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x1,
+                   const __grid_constant__ CUtensorMap tm_x2, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_y, const GroupedArgs p) {
-  using C = GroupedCfg<BMT, RS, WS>;
+  using C = GroupedCfg<BMT, RS, WS, H>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
   uint64_t* b_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -202,8 +223,8 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
   const uint32_t lane = lane_id();
   if (threadIdx.x == 0) {
     prefetch_tmap(&tm_x);
-    prefetch_tmap(&tm_x64);
-    prefetch_tmap(&tm_x128);
+    prefetch_tmap(&tm_x1);
+    prefetch_tmap(&tm_x2);
     prefetch_tmap(&tm_w);
     prefetch_tmap(&tm_y);
     for (int i = 0; i < RS; ++i) {
@@ -212,9 +233,9 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
     }
     for (int i = 0; i < WS; ++i) {
       mbar_init(&w_full[i], 1);
-      mbar_init(&w_empty[i], 8 * C::WK);   // the transform warps x the chunk's stages
+      mbar_init(&w_empty[i], 4 * H * C::WK);   // the transform warps x the chunk's stages
     }
-    for (int i = 0; i < C::AS; ++i) mbar_init(&xf_full[i], 8);   // the transform warps
+    for (int i = 0; i < C::AS; ++i) mbar_init(&xf_full[i], 4 * H);   // the transform warps
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 8);
@@ -269,9 +290,9 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
             ok = false;
             break;
           }
-          const uint32_t sf_bytes = 1024 * min(C::WK, p.num_kst - C::WK * c);
+          const uint32_t sf_bytes = 512 * min(4, p.k_atoms - 4 * c);
           mbar_arrive_expect_tx(&w_full[w.slot], C::W_BYTES + sf_bytes);
-          tma_load_2d(smem + C::OFF_W + w.slot * C::W_BYTES, &tm_w, &w_full[w.slot], c * (C::WK * C::BK / 2), wrow);
+          tma_load_2d(smem + C::OFF_W + w.slot * C::W_BYTES, &tm_w, &w_full[w.slot], c * 128, wrow);
           bulk_load(smem + C::OFF_SF + w.slot * C::SF_BYTES, sf + static_cast<size_t>(c) * C::SF_BYTES, sf_bytes,
                     &w_full[w.slot]);
         }
@@ -287,18 +308,21 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
       bool ok = true;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
         const GroupedTile g = cur.at(t, p.tiles_n, BMT);
-        // the smallest of the boxes of 64, 128 and BMT rows that covers the tile
-        const CUtensorMap* tm = g.n > 128 ? &tm_x : g.n > 64 ? &tm_x128 : &tm_x64;
-        const uint32_t bytes = 256 * (g.n > 128 ? BMT : g.n > 64 ? 128 : 64);
+        // the smallest box that covers the tile
+        const CUtensorMap* tm = g.n > C::BOX1 ? &tm_x : g.n > C::BOX2 ? &tm_x1 : &tm_x2;
+        const uint32_t piece = 128 * (g.n > C::BOX1 ? BMT : g.n > C::BOX2 ? C::BOX1 : C::BOX2);
         for (int ks = 0; ks < p.num_kst; ++ks, ++it, b.advance()) {
           if (!wait_or_abort(&b_empty[b.slot], b.phase ^ 1, p.wait_limit, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&b_full[b.slot], bytes);
+          const int pieces = min(H, p.k_atoms - H * ks);
+          mbar_arrive_expect_tx(&b_full[b.slot], piece * pieces);
           uint8_t* dst = smem + C::OFF_B + b.slot * C::B_BYTES;
-          tma_load_2d(dst, tm, &b_full[b.slot], ks * C::BK, g.row0);
-          tma_load_2d(dst + C::HALF_BYTES, tm, &b_full[b.slot], ks * C::BK + 64, g.row0);
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (h < pieces)
+              tma_load_2d(dst + h * C::PIECE_BYTES, tm, &b_full[b.slot], ks * C::BK + 64 * h, g.row0);
         }
       }
       if (!ok) fail_timeout(p.status, abort_flag);
@@ -330,11 +354,17 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
           tc_fence_after();
           // the descriptor's address field counts 16-byte units and has room for all of shared memory
           const uint64_t bdesc = bdesc0 + static_cast<uint32_t>(b.slot * (C::B_BYTES >> 4));
-          const uint32_t a_tmem = a_slots + 64 * a.slot;
+          const uint32_t a_tmem = a_slots + C::ACOLS * a.slot;
+          const int pieces = min(H, p.k_atoms - H * ks);
 #pragma unroll
-          for (int i = 0; i < C::BK / 16; ++i) {
-            tc_mma_f16_ts(d_tmem, a_tmem + 8 * i, bdesc + (i >> 2) * (C::HALF_BYTES >> 4) + 2 * (i & 3), idesc, accumulate);
-            accumulate = 1;
+          for (int h = 0; h < H; ++h) {
+            if (h < pieces) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                tc_mma_f16_ts(d_tmem, a_tmem + 32 * h + 8 * i, bdesc + h * (C::PIECE_BYTES >> 4) + 2 * i, idesc, accumulate);
+                accumulate = 1;
+              }
+            }
           }
           tc_commit(&b_empty[b.slot]);   // frees the activation stage and the A slot
         }
@@ -348,7 +378,7 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
     // ------------------------------------------------------------ transform
     const uint32_t q = static_cast<uint32_t>(warp & 3);
     const uint32_t row = 32 * q + lane;
-    const int half = (warp - 4) >> 2;     // of the stage's K elements
+    const int piece = (warp - 4) >> 2;    // of the stage's K elements
     int it = 0;
     RingPos<C::AS> a;
     RingPos<RS> freed;                    // the stage whose MMAs free the slot: it - AS
@@ -360,7 +390,7 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
           ok = false;
           break;
         }
-        const int sub = 2 * (ks % C::WK) + half;   // 64-element piece of the weight chunk
+        const int sub = H * (ks % C::WK) + piece;   // 64-element piece of the weight chunk (past K: zeros)
         // scale atom: byte (row % 32) * 16 + (row / 32) * 4 + k16 holds the block scale of K block k16
         const uint32_t sb4 = *reinterpret_cast<const uint32_t*>(smem + C::OFF_SF + w.slot * C::SF_BYTES + sub * 512 +
                                                                 lane * 16 + q * 4);
@@ -372,11 +402,12 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
         uint32_t v[32];
 #pragma unroll
         for (int w8 = 0; w8 < 8; ++w8) {
-          const uint4 o = fp4x8_scaled_to_f16(cw[w8], (sb4 >> (8 * (w8 >> 1))) & 0xFFu);
-          v[4 * w8] = o.x;
-          v[4 * w8 + 1] = o.y;
-          v[4 * w8 + 2] = o.z;
-          v[4 * w8 + 3] = o.w;
+          const __half2 s2 = e4m3x2_to_f16(w8 < 4 ? sb4 : sb4 >> 16);       // scales of words w8 & 4 .. + 3, two words each
+          const __half2 s = (w8 & 2) ? __high2half2(s2) : __low2half2(s2);
+          uint32_t h[4];
+          fp4x8_to_f16(cw[w8], h);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * w8 + j] = h2_bits(__hmul2(bits_h2(h[j]), s));
         }
         // the weights are widened in registers before the slot is waited for,
         // so a slot's turn-around is only the store
@@ -385,7 +416,7 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
           break;
         }
         tc_fence_after();
-        tmem_st32(a_slots + ((32 * q) << 16) + 64 * a.slot + 32 * half, v);
+        tmem_st32(a_slots + ((32 * q) << 16) + C::ACOLS * a.slot + 32 * piece, v);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -473,21 +504,21 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS>::THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int BMT, int RS, int WS>
+template <int BMT, int RS, int WS, int H>
 static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                                     const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
                                     int* status) {
-  using C = GroupedCfg<BMT, RS, WS>;
+  using C = GroupedCfg<BMT, RS, WS, H>;
   const int N = w->N, K = w->K;
   const int64_t x_rows = rows != nullptr ? T : rows_a;
   auto x_map = [&](CUtensorMap* map, int box_rows) {
     return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, x_rows, static_cast<int64_t>(K) * 2, 64, box_rows,
                         CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  CUtensorMap tx, tx64, tx128, tw, ty;
-  if (!x_map(&tx, BMT) || !x_map(&tx64, 64) || !x_map(&tx128, 128) ||
+  CUtensorMap tx, tx1, tx2, tw, ty;
+  if (!x_map(&tx, BMT) || !x_map(&tx1, C::BOX1) || !x_map(&tx2, C::BOX2) ||
       !make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, w->codes, K / 2, static_cast<int64_t>(w->E) * N, K / 2,
-                    C::WK * C::BK / 2, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                    128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, N, T, static_cast<int64_t>(N) * 2, 32, 32,
                     CU_TENSOR_MAP_SWIZZLE_NONE))
     return QL_ERR_CUDA;
@@ -507,7 +538,7 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   p.N = N;
   p.K = K;
   p.tiles_n = (N + 127) / 128;
-  p.num_kst = K / C::BK;
+  p.num_kst = (K + C::BK - 1) / C::BK;
   p.k_atoms = K / 64;
   p.alpha_mul = w->hadamard ? (1.0f / 128.0f) : 1.0f;
   p.wait_limit = limits.wait_limit;
@@ -516,10 +547,10 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   const int64_t e = std::min<int64_t>(w->E, T);
   const int64_t tiles = (e + (T - e) / BMT) * p.tiles_n;
   if (tiles > 0x7FFFFFFF - num_sms()) return QL_ERR_UNSUPPORTED_SHAPE;
-  auto kern = k_gemm_grouped<BMT, RS, WS>;
+  auto kern = k_gemm_grouped<BMT, RS, WS, H>;
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return QL_ERR_CUDA;
   const int grid = static_cast<int>(std::min<int64_t>(tiles, num_sms()));
-  if (launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, st, 1, tx, tx64, tx128, tw, ty, p) != cudaSuccess) {
+  if (launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, st, 1, tx, tx1, tx2, tw, ty, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return QL_ERR_CUDA;
   }
@@ -563,7 +594,17 @@ ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows
     }
     x = gathered;
   }
-  return launch_grouped_cfg<192, 3, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+  // Tile height by the rows per expert: a tall tile widens the weights once
+  // for more rows, a low one leaves room for longer K stages and a deeper
+  // weight ring.  64 experts 1408 x 2048 at 32 / 64 / 128 rows each: 64-row
+  // tiles 36 / 51 / 70 us, 128-row 40 / 42 / 61, 192-row 48 / 49 / 54; 32
+  // experts 1920 x 7680 at 32 / 64 / 128: 79 / 97 / 164, 95 / 97 / 128,
+  // 121 / 123 / 131.
+  if (T <= 40 * static_cast<int64_t>(w->E))
+    return launch_grouped_cfg<64, 3, 4, 4>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+  if (T <= 100 * static_cast<int64_t>(w->E))
+    return launch_grouped_cfg<128, 4, 3, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+  return launch_grouped_cfg<192, 3, 2, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
 }
 
 }  // namespace ql

@@ -456,6 +456,27 @@ __device__ __forceinline__ uint4 fp4x8_scaled_to_f16(uint32_t codes, uint32_t sb
   return r;
 }
 
+__device__ __forceinline__ uint32_t h2_bits(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+__device__ __forceinline__ __half2 bits_h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+
+// Eight E2M1 codes -> four f16x2 words of their values (hardware convert).
+__device__ __forceinline__ void fp4x8_to_f16(uint32_t codes, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+      "mov.b32 {c0, c1, c2, c3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, c0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, c1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, c3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+}
+// The two E4M3 scales in the low half of `v`.
+__device__ __forceinline__ __half2 e4m3x2_to_f16(uint32_t v) {
+  uint32_t s;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"(static_cast<uint16_t>(v)));
+  return bits_h2(s);
+}
+
 // Offset of block-scale j of row r in the MMA layout (512-byte atoms).
 __device__ __forceinline__ size_t sf_mma_offset(int64_t r, int32_t j, int32_t k_atoms) {
   return (static_cast<size_t>(r >> 7) * k_atoms + (j >> 2)) * 512 + (r & 31) * 16 +
