@@ -44,7 +44,7 @@ struct NormArgs {
   int64_t M;
   int32_t K, hadamard, qmax;
   int32_t warps_per_row, rows_per_cta;
-  double eps, k_inv_den;        // k_inv_den = K (the mean's divisor)
+  double eps, k_inv;            // k_inv = 1 / K
 };
 
 enum NormOut { kOutInt8 = 0, kOutF16 = 1, kOutBf16 = 2 };
@@ -97,6 +97,21 @@ __device__ __forceinline__ float rsqrt_f64(double v) {
   return static_cast<float>(1.0 / sqrt(v));
 }
 
+// Two bf16 sums, each the exact sum rounded once.  (Rounding it to fp32
+// first gives the same: a sum of two 8-bit significands that lies near a
+// bf16 border has at most 17 bits and is exact in fp32.)
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 s = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&s);
+}
+
+// RN(x inv) + 1.5 2^23, whose low mantissa bits are rint(RN(x inv)) for a
+// product below 2^22 (here at most qmax + 1/2): full-rate adds where the
+// float-to-int conversion runs at an eighth of it.  The product is rounded by
+// itself (the _rn intrinsics are not contracted).
+constexpr float kRoundMagic = 12582912.0f;
+__device__ __forceinline__ float round_magic(float x, float inv) { return __fadd_rn(__fmul_rn(x, inv), kRoundMagic); }
+
 // Barrier of one row's warps.
 __device__ __forceinline__ void row_sync(int row_slot, int warps) {
   if (warps == 1) __syncwarp();
@@ -106,14 +121,14 @@ __device__ __forceinline__ void row_sync(int row_slot, int warps) {
 }  // namespace
 
 template <int V, int OUT>
-__global__ void __launch_bounds__(kNormMaxThreads, V == 1 ? 2 : 1) k_norm_quantize(const NormArgs p) {
+__global__ void __launch_bounds__(kNormMaxThreads, V <= 2 ? 2 : 1) k_norm_quantize(const NormArgs p) {
   __shared__ double s_sum[kNormMaxThreads / 32];
   __shared__ float s_max[kNormMaxThreads / 32];
-  const int warps = p.warps_per_row;
-  const int warp = threadIdx.x >> 5;
+  const int warps = p.warps_per_row;             // blockDim.x / 32
   const uint32_t lane = lane_id();
-  const int slot = warp / warps;                 // row of this CTA
-  const int t = static_cast<int>(threadIdx.x) - slot * 32 * warps;   // thread within the row
+  const int slot = threadIdx.y;                  // row of this CTA
+  const int t = threadIdx.x;                     // thread within the row
+  const int warp = slot * warps + (t >> 5);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * p.rows_per_cta + slot;
   pdl_wait();
   if (row < p.M) {                               // uniform over the row's warps
@@ -151,8 +166,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, V == 1 ? 2 : 1) k_norm_quanti
           uint32_t* hw = reinterpret_cast<uint32_t*>(&h[v][c]);
           const uint32_t* rw = reinterpret_cast<const uint32_t*>(&r[v][c]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            hw[i] = pack_bf16x2(__fadd_rn(bf16_lo(hw[i]), bf16_lo(rw[i])), __fadd_rn(bf16_hi(hw[i]), bf16_hi(rw[i])));
+          for (int i = 0; i < 4; ++i) hw[i] = add_bf16x2(hw[i], rw[i]);
           if (p.residual_out != nullptr && active(v))
             *reinterpret_cast<uint4*>(p.residual_out + 2 * (base + offset(v)) + 128 * c) = h[v][c];
         }
@@ -179,7 +193,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, V == 1 ? 2 : 1) k_norm_quanti
       sum = 0.0;
       for (int w = 0; w < warps; ++w) sum += s_sum[slot * warps + w];
     }
-    const float rstd = rsqrt_f64(sum / p.k_inv_den + p.eps);
+    const float rstd = rsqrt_f64(sum * p.k_inv + p.eps);
 
     float2 P[V][8];
     float m = 0.f;
@@ -235,29 +249,25 @@ __global__ void __launch_bounds__(kNormMaxThreads, V == 1 ? 2 : 1) k_norm_quanti
       for (int v = 0; v < V; ++v) {
         if (!active(v)) continue;
         const int64_t o = base + offset(v);
-        float2 q[8];
+        float2 q[8];   // rounded codes plus the magic constant
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = __fmul2_rn(P[v][j], make_float2(inv, inv));
+        for (int j = 0; j < 8; ++j) q[j] = make_float2(round_magic(P[v][j].x, inv), round_magic(P[v][j].y, inv));
         if constexpr (OUT == kOutF16) {
-          // rint, -0 to +0, two codes per f16x2 convert (integers up to 127: exact)
+          // the code itself (zero as +0), two per f16x2 convert (integers up to 127: exact)
           uint4 c[2];
           uint32_t* c0 = reinterpret_cast<uint32_t*>(&c[0]);
           uint32_t* c1 = reinterpret_cast<uint32_t*>(&c[1]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const __half2 a = __floats2half2_rn(__fadd_rn(rintf(q[2 * i].x), 0.f), __fadd_rn(rintf(q[2 * i + 1].x), 0.f));
-            const __half2 b = __floats2half2_rn(__fadd_rn(rintf(q[2 * i].y), 0.f), __fadd_rn(rintf(q[2 * i + 1].y), 0.f));
-            c0[i] = *reinterpret_cast<const uint32_t*>(&a);
-            c1[i] = *reinterpret_cast<const uint32_t*>(&b);
+            c0[i] = h2_bits(__floats2half2_rn(__fsub_rn(q[2 * i].x, kRoundMagic), __fsub_rn(q[2 * i + 1].x, kRoundMagic)));
+            c1[i] = h2_bits(__floats2half2_rn(__fsub_rn(q[2 * i].y, kRoundMagic), __fsub_rn(q[2 * i + 1].y, kRoundMagic)));
           }
           *reinterpret_cast<uint4*>(p.codes + 2 * o) = c[0];
           *reinterpret_cast<uint4*>(p.codes + 2 * o + 128) = c[1];
         } else {
           auto pack4 = [](float a0, float a1, float a2, float a3) {
-            const uint32_t lo = __byte_perm(static_cast<uint32_t>(__float2int_rn(a0)),
-                                            static_cast<uint32_t>(__float2int_rn(a1)), 0x0040);
-            const uint32_t hi = __byte_perm(static_cast<uint32_t>(__float2int_rn(a2)),
-                                            static_cast<uint32_t>(__float2int_rn(a3)), 0x0040);
+            const uint32_t lo = __byte_perm(__float_as_uint(a0), __float_as_uint(a1), 0x0040);   // the low bytes
+            const uint32_t hi = __byte_perm(__float_as_uint(a2), __float_as_uint(a3), 0x0040);
             return __byte_perm(lo, hi, 0x5410);
           };
           *reinterpret_cast<uint2*>(p.codes + o) =
@@ -276,9 +286,13 @@ ql_status launch_norm_quantize(const void* x, const void* residual, const void* 
                                float* scales, cudaStream_t st) {
   if (M == 0) return QL_OK;
   if (K > 4 * 16 * kNormMaxThreads) return QL_ERR_UNSUPPORTED_SHAPE;
-  // one vector per thread up to K = 8192 (the most threads, the shortest
-  // dependent chain), then two or four
-  const int V = K <= 16 * kNormMaxThreads ? 1 : K <= 2 * 16 * kNormMaxThreads ? 2 : 4;
+  // Vectors per thread: two where rows fill the GPU and have the threads for
+  // it (per row and warp the reductions, the root and the divisions cost as
+  // much as a vector: 17776 x 1920 to int8 43.6 against 51.5 us, 17776 x 7680
+  // 165 against 244), one for few or short rows (one row of 5120: 3.0 us in
+  // 10 warps; 65536 x 256 42 against 65 us), four beyond 16384 elements.
+  const bool one = K <= 16 * kNormMaxThreads && (K < 1024 || M < num_sms());
+  const int V = one ? 1 : K <= 2 * 16 * kNormMaxThreads ? 2 : 4;
   NormArgs p{};
   p.x = static_cast<const uint8_t*>(x);
   p.residual = static_cast<const uint8_t*>(residual);
@@ -292,7 +306,7 @@ ql_status launch_norm_quantize(const void* x, const void* residual, const void* 
   p.hadamard = hadamard;
   p.qmax = qmax;
   p.eps = static_cast<double>(eps);
-  p.k_inv_den = static_cast<double>(K);
+  p.k_inv = 1.0 / static_cast<double>(K);
   p.warps_per_row = (K / 16 + 32 * V - 1) / (32 * V);
   p.rows_per_cta = std::max(1, 8 / p.warps_per_row);   // short rows share a CTA of up to 8 warps
   const int64_t grid = (M + p.rows_per_cta - 1) / p.rows_per_cta;
@@ -300,7 +314,7 @@ ql_status launch_norm_quantize(const void* x, const void* residual, const void* 
   if (out_kind == kOutInt8) kern = V == 1 ? k_norm_quantize<1, kOutInt8> : V == 2 ? k_norm_quantize<2, kOutInt8> : k_norm_quantize<4, kOutInt8>;
   if (out_kind == kOutF16) kern = V == 1 ? k_norm_quantize<1, kOutF16> : V == 2 ? k_norm_quantize<2, kOutF16> : k_norm_quantize<4, kOutF16>;
   if (out_kind == kOutBf16) kern = V == 1 ? k_norm_quantize<1, kOutBf16> : V == 2 ? k_norm_quantize<2, kOutBf16> : k_norm_quantize<4, kOutBf16>;
-  if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(32 * p.warps_per_row * p.rows_per_cta), 0, st, 1, p) !=
+  if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(32 * p.warps_per_row, p.rows_per_cta), 0, st, 1, p) !=
       cudaSuccess) {
     (void)cudaGetLastError();
     return QL_ERR_CUDA;

@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-__device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31; }
+__device__ __forceinline__ uint32_t lane_id() { return threadIdx.x & 31; }   // blockDim.x a multiple of 32
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;

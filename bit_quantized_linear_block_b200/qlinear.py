@@ -154,12 +154,12 @@ def _stream(stream, device):
 
 def _call_on(device, stream, *inputs):
     """A context for one call on `device`: new tensors belong to the stream
-    that the call runs on, and when that is not the current stream the
-    inputs' memory is kept until the call is done with it."""
+    that the call runs on, and when that is not the current stream the memory
+    of the given ones is kept until the call is done with it."""
     if stream is None:
         return nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
     for t in inputs:
-        if t is not None:
+        if t is not None and t.is_cuda:
             t.record_stream(stream)
     return torch.cuda.stream(stream)
 
@@ -544,9 +544,9 @@ def qlinear_norm_quantize(X: torch.Tensor, gamma: torch.Tensor, act_fmt: int = Q
     if plain and keep_norm:
         raise ValueError("keep_norm: QL_ROUTE_BF16 already returns the norm as its codes")
     st = _stream(stream, dev)
-    with _call_on(dev, stream, X, gamma, residual):
+    with _call_on(dev, stream, X, gamma, residual, *(out or {}).values()):
         if out is None:
-            codes = torch.empty((M, K), dtype=_NORM_DTYPES[act_fmt], device=dev)
+            codes = torch.empty_like(X, dtype=_NORM_DTYPES[act_fmt])
             scales = None if plain else torch.empty(max(M, 1), dtype=torch.float32, device=dev)
             h = None if residual is None else torch.empty_like(X)
             y = torch.empty_like(X) if keep_norm else None
@@ -615,13 +615,15 @@ def qlinear_gemv(act_fmt: int, q: dict, M: int, w: PackedWeights, Y: torch.Tenso
     dtype = _GEMV_DTYPES.get(act_fmt)
     if dtype is None:
         raise ValueError(f"activation format {act_fmt} has no form for few rows")
-    codes = _tensor(q["codes"], "q['codes']", dtype, w.buf.device, M * w.K * dtype.itemsize)
-    dev = codes.device
+    dev = w.buf.device
+    codes = _tensor(q["codes"], "q['codes']", dtype, dev, dim=2)
+    if codes.shape[0] < M or codes.shape[1] != w.K:
+        raise ValueError(f"q['codes'] is {tuple(codes.shape)}, the call reads {(M, w.K)}")
     scales = None
     if act_fmt != QL_ROUTE_BF16:
         scales = _tensor(q["scales"], "q['scales']", torch.float32, dev, 4 * M)
     st = _stream(stream, dev)
-    with _call_on(dev, stream, codes, scales, w.buf):
+    with _call_on(dev, stream, codes, scales, w.buf, Y):
         Y = _output(Y, M, w.N, dev)
         _check("qlinear_gemv", lib.qlinear_gemv(act_fmt, _ptr(codes), _ptr(scales), M, C.byref(w.desc), _ptr(Y), st))
     return Y
@@ -683,7 +685,7 @@ def qlinear_grouped_gemm(act_fmt: int, q: dict, offsets: torch.Tensor, w: Packed
     if ws is not None:
         _tensor(ws, "ws", torch.uint8, dev)
     st = _stream(stream, dev)
-    with _call_on(dev, stream, codes, scales, offsets, rows, w.buf):
+    with _call_on(dev, stream, codes, scales, offsets, rows, w.buf, Y, ws):
         if Y is None:
             Y = torch.empty((T, w.N), dtype=torch.bfloat16, device=dev)
         if ws is None and rows is not None:
