@@ -32,9 +32,8 @@
 // significant bits against the 8 of the bf16 output, and exact for an
 // unrotated block's bf16 values down to 2^-29 of its largest; the block's
 // sums are scaled back in fp32.
-#include <mutex>
+#include <atomic>
 #include <type_traits>
-#include <unordered_map>
 
 #include "ql_common.cuh"
 #include "gemm_common.cuh"
@@ -367,7 +366,7 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
         }
       }
       // All four tiles, step by step, so that their chains of dependent MMAs
-      // overlap (tile by tile a block took about XX% longer).  A tile past N
+      // overlap (a tile at a time, each waits for its own eight).  A tile past N
       // multiplies what its ring slot happens to hold; nothing of it is stored.
       uint4 ca[4], cb[4];
 #pragma unroll
@@ -514,19 +513,14 @@ int gemv_units(int32_t N) {
   return 2 * (N / 128) + (r == 0 ? 0 : r > 16 ? 2 : 1);
 }
 
-// Warps of this kernel that an SM's registers hold.
-int gemv_warps_per_sm(const void* kern) {
-  static std::mutex mu;
-  static std::unordered_map<const void*, int> known;
-  std::lock_guard<std::mutex> lk(mu);
-  const auto it = known.find(kern);
-  if (it != known.end()) return it->second;
+// Warps of a kernel that an SM's registers hold.
+int warps_per_sm(const void* kern) {
   cudaFuncAttributes a;
   if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) {
     (void)cudaGetLastError();
     return 8;
   }
-  return known[kern] = 65536 / (32 * ((a.numRegs + 7) / 8 * 8));
+  return 65536 / (32 * ((a.numRegs + 7) / 8 * 8));
 }
 
 // tiles: row tiles (grouped: the most that the experts' rows can make).
@@ -544,7 +538,9 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   // partial sums), as far as two CTAs (one, if that is all an SM gets) stay
   // resident together: 16 rows x 15360 x 5120 took 19.5 us in one wave of 6
   // warps a CTA and 24.2 in two of 8.
-  const int reg_warps = gemv_warps_per_sm(reinterpret_cast<const void*>(kern));
+  static std::atomic<int> known{0};   // the same for every device
+  int reg_warps = known.load(std::memory_order_relaxed);
+  if (reg_warps == 0) known.store(reg_warps = warps_per_sm(reinterpret_cast<const void*>(kern)), std::memory_order_relaxed);
   auto sm_ctas = [&](int S) { return (ctas * S + num_sms() - 1) / num_sms(); };   // of the fullest SM
   auto warps_for = [&](int S) {
     const int64_t together = std::min<int64_t>(sm_ctas(S), 2);

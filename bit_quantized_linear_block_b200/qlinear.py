@@ -569,7 +569,7 @@ def qlinear_norm_quantize(X: torch.Tensor, gamma: torch.Tensor, act_fmt: int = Q
 
 def _output(Y, M: int, N: int, dev):
     if Y is None:
-        return torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        return torch.empty(M, N, dtype=torch.bfloat16, device=dev)
     return _tensor(Y, "Y", torch.bfloat16, dev, 2 * M * N)
 
 
@@ -687,7 +687,7 @@ def qlinear_grouped_gemm(act_fmt: int, q: dict, offsets: torch.Tensor, w: Packed
     st = _stream(stream, dev)
     with _call_on(dev, stream, codes, scales, offsets, rows, w.buf, Y, ws):
         if Y is None:
-            Y = torch.empty((T, w.N), dtype=torch.bfloat16, device=dev)
+            Y = torch.empty(T, w.N, dtype=torch.bfloat16, device=dev)
         if ws is None and rows is not None:
             need = lib.qlinear_grouped_gemm_ws_bytes(T, C.byref(w.desc), 1)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None

@@ -218,11 +218,12 @@ def test_a_decoder_block_in_one_graph(ql, tokens):
     del graphs
 
 
-def test_a_wait_that_runs_out_is_reported(ql):
+@pytest.mark.parametrize("counts", [[20, 30, 40], [60, 100, 80], [200, 150, 250]])    # the three tile heights
+def test_a_wait_that_runs_out_is_reported(ql, counts):
     w, _ = _experts(ql, 3, 512, 1920, 16)
-    q = _tokens(ql, 600, 1920, 17)
-    off = _offsets([200, 150, 250])
-    for rows in (None, torch.arange(600, dtype=torch.int32, device="cuda")):
+    q = _tokens(ql, sum(counts), 1920, 17)
+    off = _offsets(counts)
+    for rows in (None, torch.arange(sum(counts), dtype=torch.int32, device="cuda")):
         want = ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, off, w, rows=rows)
         torch.cuda.synchronize()
         ql.qlinear_debug_set_wait_limit(0)
