@@ -264,7 +264,7 @@ bool make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                   CUtensorMapSwizzle swizzle);
 bool make_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, int64_t d0, int64_t d1,
                   int64_t d2, int64_t stride1_bytes, int64_t stride2_bytes, uint32_t b0, uint32_t b1,
-                  uint32_t b2);
+                  uint32_t b2, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
 // Block scales in the MMA layout as a 3-D tensor of 32-bit words
 // (128 words of a 512-byte atom, K/64 atoms of a 128-row group, row groups);
 // one box is box_k atoms (4 = one 256-value K stage) of one group.

@@ -25,7 +25,7 @@
 //   warp 0      weight producer: 256-deep K chunks of the FP4 tile (128-byte
 //               rows, 128-byte swizzle) and their scales by TMA, WS-deep ring;
 //   warp 1      TMEM allocator and MMA issuer (kind::f16, A from tensor memory);
-//   warp 2      activation producer: a stage is one TMA box of rows per piece,
+//   warp 2      activation producer: a stage is one 3-D TMA box, rows x pieces,
 //               of the smallest of three heights that covers the tile, RS-deep
 //               ring;
 //   4 H warps   transform: four warps widen piece h of every stage, lane l of
@@ -93,8 +93,7 @@ struct GroupedCfg {
   static constexpr int AS = FREE < RS ? FREE : RS; // A slots
   static constexpr int BOX1 = BMT == 192 ? 128 : BMT / 2;   // smaller activation boxes
   static constexpr int BOX2 = BMT == 192 ? 64 : BMT / 4;
-  static constexpr int PIECE_BYTES = BMT * 128;    // 64 f16 of K per row
-  static constexpr int B_BYTES = H * PIECE_BYTES;
+  static constexpr int B_BYTES = H * BMT * 128;    // 64 f16 of K per row and piece
   static constexpr int W_BYTES = 128 * 128;
   static constexpr int SF_BYTES = 4 * 512;
   static constexpr int OFF_B = 0;
@@ -106,11 +105,12 @@ struct GroupedCfg {
   static constexpr int NBAR = 2 * RS + 2 * WS + AS + 2 * 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
+  static constexpr __host__ __device__ int box_rows(int n) { return n > BOX1 ? BMT : n > BOX2 ? BOX1 : BOX2; }
   static constexpr int EPI0 = 4 + 4 * H;           // first epilogue warp
   static constexpr int THREADS = (EPI0 + 8) * 32;
   static_assert(AS >= 2, "tensor memory budget");
   static_assert(H == 2 || H == 4, "a weight chunk is two stages or one");
-  static_assert(PIECE_BYTES % 1024 == 0 && BOX2 % 8 == 0, "whole swizzle atoms");
+  static_assert(BOX2 % 8 == 0, "whole swizzle atoms");
   static_assert(OFF_BAR % 8 == 0, "mbarrier alignment");
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -310,19 +310,14 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, H>::THREADS, 1)
         const GroupedTile g = cur.at(t, p.tiles_n, BMT);
         // the smallest box that covers the tile
         const CUtensorMap* tm = g.n > C::BOX1 ? &tm_x : g.n > C::BOX2 ? &tm_x1 : &tm_x2;
-        const uint32_t piece = 128 * (g.n > C::BOX1 ? BMT : g.n > C::BOX2 ? C::BOX1 : C::BOX2);
+        const uint32_t bytes = 128 * H * C::box_rows(g.n);
         for (int ks = 0; ks < p.num_kst; ++ks, ++it, b.advance()) {
           if (!wait_or_abort(&b_empty[b.slot], b.phase ^ 1, p.wait_limit, abort_flag)) {
             ok = false;
             break;
           }
-          const int pieces = min(H, p.k_atoms - H * ks);
-          mbar_arrive_expect_tx(&b_full[b.slot], piece * pieces);
-          uint8_t* dst = smem + C::OFF_B + b.slot * C::B_BYTES;
-#pragma unroll
-          for (int h = 0; h < H; ++h)
-            if (h < pieces)
-              tma_load_2d(dst + h * C::PIECE_BYTES, tm, &b_full[b.slot], ks * C::BK + 64 * h, g.row0);
+          mbar_arrive_expect_tx(&b_full[b.slot], bytes);
+          tma_load_3d(smem + C::OFF_B + b.slot * C::B_BYTES, tm, &b_full[b.slot], 0, g.row0, H * ks);
         }
       }
       if (!ok) fail_timeout(p.status, abort_flag);
@@ -337,7 +332,9 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, H>::THREADS, 1)
       const uint64_t bdesc0 = smem_desc(smem_u32(smem + C::OFF_B), 0, 1024, kSwizzle128B);
       bool ok = true;
       for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x, d.advance()) {
-        const uint32_t idesc = grouped_idesc(cur.at(t, p.tiles_n, BMT).n);
+        const int n = cur.at(t, p.tiles_n, BMT).n;
+        const uint32_t idesc = grouped_idesc(n);
+        const uint32_t piece = static_cast<uint32_t>(C::box_rows(n) * 128 >> 4);   // from one piece of a stage to the next
         if (!wait_or_abort(&tempty[d.slot], d.phase ^ 1, p.wait_limit, abort_flag)) {
           ok = false;
           break;
@@ -361,7 +358,7 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, H>::THREADS, 1)
             if (h < pieces) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                tc_mma_f16_ts(d_tmem, a_tmem + 32 * h + 8 * i, bdesc + h * (C::PIECE_BYTES >> 4) + 2 * i, idesc, accumulate);
+                tc_mma_f16_ts(d_tmem, a_tmem + 32 * h + 8 * i, bdesc + h * piece + 2 * i, idesc, accumulate);
                 accumulate = 1;
               }
             }
@@ -511,9 +508,10 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   using C = GroupedCfg<BMT, RS, WS, H>;
   const int N = w->N, K = w->K;
   const int64_t x_rows = rows != nullptr ? T : rows_a;
-  auto x_map = [&](CUtensorMap* map, int box_rows) {
-    return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, K, x_rows, static_cast<int64_t>(K) * 2, 64, box_rows,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
+  // 64 values x rows x pieces of K: one box brings all pieces of a stage
+  auto x_map = [&](CUtensorMap* map, uint32_t box_rows) {
+    return make_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a, 64, x_rows, K / 64, static_cast<int64_t>(K) * 2, 128, 64,
+                        box_rows, H, CU_TENSOR_MAP_SWIZZLE_128B);
   };
   CUtensorMap tx, tx1, tx2, tw, ty;
   if (!x_map(&tx, BMT) || !x_map(&tx1, C::BOX1) || !x_map(&tx2, C::BOX2) ||
