@@ -706,11 +706,12 @@ ql_status qlinear_prepare_experts(const void* W, int32_t E, int32_t N, int32_t K
 }
 
 namespace {
-// At most about one row per expert, or few rows over few experts: the form
-// that streams the weights without tensor-memory tiles (64 experts 1408 x
-// 2048: 18 against 23 us at 32 rows, 31 against 29 at 64; one expert 7680 x
-// 1920 at 16 rows: 8 us).
-bool grouped_few(int64_t T, int64_t E) { return T <= E || (T <= 16 && E <= 4); }
+// At most one row for two experts, or few rows over few experts: the form that
+// streams the weights without tensor-memory tiles (us, that form / the tiles:
+// 64 experts 1408 x 2048 at 16 / 32 / 64 rows 14 / 17, 18 / 18, 31 / 28; 32
+// experts 1920 x 7680 at 8 / 16 / 32 rows 20 / 23, 35 / 42, 43 / 42; one
+// expert 1920 x 1920 at one row 5.4 / 9.6).
+bool grouped_few(int64_t T, int64_t E) { return 2 * T <= E || (T <= 16 && E <= 4); }
 }  // namespace
 
 size_t qlinear_grouped_gemm_ws_bytes(int64_t T, const ql_experts* w, int32_t gathers) {

@@ -51,6 +51,8 @@ constexpr int kGvCodeBytes = 8 * 512;       // 4 MMA tiles x 2 row halves x 32 l
 constexpr int kGvStage = kGvCodeBytes + 2 * 512;   // + the scales of both row halves
 constexpr int kGvMaxCluster = 8;
 
+constexpr int gv_x_bytes(int nt) { return nt * (2048 + 32) + 16; }   // f16 fragments, 8 factors a tile, a zero piece
+
 enum GvAct { kGvBf16 = 0, kGvF16 = 1, kGvI8 = 2 };
 
 struct GvArgs {
@@ -209,6 +211,7 @@ template <int NT, int ACT, bool GROUPED, int ONE>
 __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(const GvArgs p) {
   constexpr int kTokens = 8 * NT;
   constexpr bool kScaled = ACT == kGvBf16;       // a factor per row and K block
+  constexpr int kXBytes = gv_x_bytes(NT), kXZero = kXBytes - 16;   // a warp's rows of `a`, then 16 zero bytes
   constexpr int kRaw = ACT == kGvI8 ? 2 : 4;     // 16-byte pieces of a lane's 32 elements
   extern __shared__ __align__(16) uint8_t smem[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
@@ -267,20 +270,29 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
   const uint8_t* ssrc = sf + (static_cast<size_t>(unit >> 1) * (p.K >> 6) + (t >> 1)) * 512 +
                         static_cast<size_t>(16 * (unit & 1) + g) * 16;
   uint8_t* ring = smem + warp * (kGvDepth * kGvStage);
-  uint8_t* xbuf = smem + warps * (kGvDepth * kGvStage) + warp * (NT * 2048 + NT * 32);
+  uint8_t* xbuf = smem + warps * (kGvDepth * kGvStage) + warp * kXBytes;
   float* xscale = reinterpret_cast<float*>(xbuf + NT * 2048);
+  if (lane == 0) *reinterpret_cast<uint4*>(xbuf + kXZero) = make_uint4(0, 0, 0, 0);   // read in place of rows that are not there
+  // This lane's pieces of block 0, moved on by a block of this warp with each
+  // issue.  Tiles past N copy tile 0 again (their sums are not stored).
+  const uint8_t* wp[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    wp[i] = wsrc + static_cast<size_t>(i < ntiles ? 32 * i : 0) * row_bytes + static_cast<size_t>(kb0 + warp) * 64;
+  const uint8_t* sp = ssrc + static_cast<size_t>(kb0 + warp) * 1024;
+  const size_t half = 8 * row_bytes;
   auto issue = [&](int j) {                      // weights and scales of block j into its ring slot
     if (j < nblk) {
-      const int kb = kb0 + warp + j * warps;
       const uint32_t dst = smem_u32(ring + (j % kGvDepth) * kGvStage) + 16 * lane;
-      for (int i = 0; i < ntiles; ++i) {
-        const uint8_t* src = wsrc + static_cast<size_t>(32 * i) * row_bytes + static_cast<size_t>(kb) * 64;
-        cp_async16(dst + (2 * i) * 512, src);
-        cp_async16(dst + (2 * i + 1) * 512, src + 8 * row_bytes);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        cp_async16(dst + (2 * i) * 512, wp[i]);
+        cp_async16(dst + (2 * i + 1) * 512, wp[i] + half);
+        wp[i] += 64 * warps;
       }
-      const uint8_t* s = ssrc + static_cast<size_t>(kb) * 1024;
-      cp_async16(dst + kGvCodeBytes, s);
-      cp_async16(dst + kGvCodeBytes + 512, s + 128);
+      cp_async16(dst + kGvCodeBytes, sp);
+      cp_async16(dst + kGvCodeBytes + 512, sp + 128);
+      sp += 1024 * warps;
     }
     cp_async_commit();                           // a group per block, empty past the end
   };
@@ -352,8 +364,8 @@ __global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(cons
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const bool mine = one ? g == 2 * t + (q >> 1) : g < m2;
-          xf[nt][q] = mine ? lds128(xbuf + nt * 2048 + q * 512 + (one ? 4 * b + t : b * m2 * 4 + lane) * 16)
-                           : make_uint4(0, 0, 0, 0);
+          const int at = nt * 2048 + q * 512 + (one ? 4 * b + t : b * m2 * 4 + lane) * 16;
+          xf[nt][q] = lds128(xbuf + (mine ? at : kXZero));
         }
       const uint4 sa = lds128(slot + kGvCodeBytes), sb = lds128(slot + kGvCodeBytes + 512);
       const uint32_t sa4[4] = {sa.x, sa.y, sa.z, sa.w}, sb4[4] = {sb.x, sb.y, sb.z, sb.w};
@@ -530,7 +542,7 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   const int64_t ctas = units * tiles;
   auto kern = k_gemv<NT, ACT, GROUPED, ONE>;
   auto smem_for = [&](int warps, int S) {
-    const int ring = warps * (kGvDepth * kGvStage + NT * 2048 + NT * 32);
+    const int ring = warps * (kGvDepth * kGvStage + gv_x_bytes(NT));
     const int red = 8 * NT * (warps * (kGvRows + 1) + (S > 1 ? S * kGvRows : 0)) * 4;
     return std::max(ring, red);
   };
