@@ -560,9 +560,9 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
 }
 
 // ---------------------------------------------------------------------------
-// Source rows into output order: out[r] = a[rows[r]] (row 0 for a row that
-// does not exist: the product scales it by 0).  HBM: 2 bytes per value
-// written, and read where a row is new to L2.  The product then loads whole
+// Source rows into output order: out[r] = a[rows[r]] (zeros for a row that
+// does not exist).  HBM: 2 bytes per value written, and read where a row is
+// new to L2.  The product then loads whole
 // boxes; gathering inside it was slower, since each row tile is loaded once
 // per 128 columns of Y: 17664 x 7680 x 1920 took 974 us with four-row TMA
 // gathers and 742 us with 16-byte asynchronous copies, against 388 us for
@@ -574,10 +574,12 @@ __global__ void __launch_bounds__(kThreadsHbm) k_gather_rows(const uint4* a, con
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreadsHbm / 32);
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreadsHbm / 32) + (threadIdx.x >> 5); r < T; r += step) {
     const int32_t v = rows[r];
-    const uint4* src = a + (v >= 0 && v < rows_a ? v : 0) * static_cast<int64_t>(pieces);
+    const bool ok = v >= 0 && v < rows_a;
+    const uint4* src = a + static_cast<int64_t>(ok ? v : 0) * pieces;
     uint4* dst = out + r * pieces;
 #pragma unroll 4
-    for (int32_t i = static_cast<int32_t>(lane_id()); i < pieces; i += 32) dst[i] = src[i];
+    for (int32_t i = static_cast<int32_t>(lane_id()); i < pieces; i += 32)
+      dst[i] = ok ? src[i] : make_uint4(0, 0, 0, 0);
   }
   pdl_release();
 }

@@ -391,8 +391,9 @@ QL_API ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_sca
    captured; replays follow the values that they then hold.  Rows of Y outside
    every segment are left as they are.  An offset outside [0, T] counts as the
    nearer end, and one below an earlier offset as that offset (an empty
-   segment); a source row outside [0, rows_a) gives a row of zeros.  Y must not overlap an operand.
-   4-byte aligned offsets and row_index.  ws: qlinear_grouped_gemm_ws_bytes(T,
+   segment); a source row outside [0, rows_a) gives a row of zeros.  A row
+   with non-finite values affects only the rows of Y that it is the source of.
+   Y must not overlap an operand.  4-byte aligned offsets and row_index.  ws: qlinear_grouped_gemm_ws_bytes(T,
    w, row_index != NULL) bytes of scratch (0: ws may be NULL), 256-byte
    aligned, not initialized; calls in flight at once need one each. */
 QL_API size_t qlinear_experts_bytes(int32_t E, int32_t N, int32_t K);

@@ -160,6 +160,52 @@ def test_offsets_and_rows_out_of_range(ql, total):
     assert ql.qlinear_device_status() == 0
 
 
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts", [[3, 0, 5], [20, 30, 40], [60, 0, 100], [200, 150, 250]])   # every form
+def test_a_bad_row_stays_alone(ql, counts, gather):
+    """NaN and infinite codes in rows inside and behind the segments, and in
+    row 0, which stands beside the rows that do not exist."""
+    w, _ = _experts(ql, 3, 48, 256, 20)
+    T = sum(counts) + 6
+    q = _tokens(ql, T, 256, 21)
+    off = _offsets(counts, 2)
+    rows = None
+    if gather:
+        rows = torch.randint(0, T, (T,), generator=torch.Generator().manual_seed(T)).to(torch.int32).cuda()
+        rows[3::7] = -1
+    y = torch.full((T, 48), 0.25, dtype=torch.bfloat16, device="cuda")
+    want = ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, off, w, rows=rows, Y=y.clone())
+    bad = {key: v.clone() for key, v in q.items() if v is not None}
+    hit = torch.tensor([0, 4, 5, T - 1], device="cuda")
+    bad["codes"][hit[::2]] = float("nan")
+    bad["codes"][hit[1::2], 17] = float("inf")
+    got = ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, bad, off, w, rows=rows, Y=y.clone())
+    src = torch.arange(T, device="cuda") if rows is None else rows.long()
+    keep = ~torch.isin(src, hit)
+    assert bool(keep.any()) and torch.equal(got[keep], want[keep])
+    if gather:
+        inside = torch.arange(T, device="cuda")
+        inside = (inside >= 2) & (inside < 2 + sum(counts)) & (src == -1)
+        assert bool(inside.any()) and bool((got[inside] == 0).all())
+
+
+@pytest.mark.parametrize("counts", [[2, 0, 1, 4, 0, 0, 1], [40, 7, 0, 150, 33, 9, 80]])
+def test_two_calls_at_once(ql, counts):
+    """The same weights on two streams, each call with its own workspace."""
+    w, _ = _experts(ql, len(counts), 1920, 640, 22)
+    T, off, gen = sum(counts), _offsets(counts), torch.Generator().manual_seed(5)
+    qs = [_tokens(ql, 30, 640, 23 + i) for i in range(2)]
+    rows = [torch.randint(0, 30, (T,), generator=gen).to(torch.int32).cuda() for _ in range(2)]
+    want = [ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, qs[i], off, w, rows=rows[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    got = [[ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, qs[i], off, w, rows=rows[i], stream=side[i]) for i in range(2)]
+           for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(pair[i], want[i]) for pair in got for i in range(2))
+    assert ql.qlinear_device_status() == 0
+
+
 def test_empty_calls(ql):
     w, _ = _experts(ql, 2, 64, 256, 10)
     q = _tokens(ql, 4, 256, 11)
