@@ -22,7 +22,7 @@
 //     fill the GPU.  Partial sums are added in a fixed order (warps through
 //     shared memory, CTAs through distributed shared memory), so results do
 //     not depend on timing and need no workspace;
-//   * each lane copies the pieces it will read itself (cp.async, kDepth
+//   * each lane copies the pieces it will read itself (cp.async, kGvDepth
 //     blocks ahead), so the ring needs no barrier.
 //
 // MMA operands are f16: a weight value E2M1 x E4M3 (at most 6 significant
@@ -553,7 +553,8 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   static std::atomic<int> known{0};   // the same for every device
   int reg_warps = known.load(std::memory_order_relaxed);
   if (reg_warps == 0) known.store(reg_warps = warps_per_sm(reinterpret_cast<const void*>(kern)), std::memory_order_relaxed);
-  auto sm_ctas = [&](int S) { return (ctas * S + num_sms() - 1) / num_sms(); };   // of the fullest SM
+  const int sms = num_sms();
+  auto sm_ctas = [&](int S) { return (ctas * S + sms - 1) / sms; };   // of the fullest SM
   auto warps_for = [&](int S) {
     const int64_t together = std::min<int64_t>(sm_ctas(S), 2);
     int warps = std::max(4, std::min(kGvMaxWarps, (kb + S - 1) / S));

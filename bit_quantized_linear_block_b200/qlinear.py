@@ -132,7 +132,7 @@ def _check(fn: str, status: int):
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()      # an int: argtypes make it a pointer
 
 
 # The handle of a device's current stream without making a Stream object
@@ -159,7 +159,7 @@ def _call_on(device, stream, *inputs):
     if stream is None:
         return nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
     for t in inputs:
-        if t is not None and t.is_cuda:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
             t.record_stream(stream)
     return torch.cuda.stream(stream)
 
@@ -554,12 +554,12 @@ def qlinear_norm_quantize(X: torch.Tensor, gamma: torch.Tensor, act_fmt: int = Q
             codes = _tensor(out["codes"], "out['codes']", _NORM_DTYPES[act_fmt], dev,
                             M * K * _NORM_DTYPES[act_fmt].itemsize)
             scales = None if plain else _tensor(out["scales"], "out['scales']", torch.float32, dev, 4 * M)
-            h = None if residual is None else out.get("residual")
-            y = out.get("norm") if keep_norm else None
-            if h is not None:
-                _tensor(h, "out['residual']", torch.bfloat16, dev, 2 * M * K)
-            if keep_norm:
-                _tensor(y, "out['norm']", torch.bfloat16, dev, 2 * M * K)
+            def reuse(name):      # made here when the earlier call had none
+                t = out.get(name)
+                return torch.empty_like(X) if t is None else _tensor(t, f"out['{name}']", torch.bfloat16, dev, 2 * M * K)
+
+            h = None if residual is None else reuse("residual")
+            y = reuse("norm") if keep_norm else None
         _check("qlinear_norm_quantize",
                lib.qlinear_norm_quantize(_ptr(X), _ptr(residual), _ptr(gamma), M, K, eps, act_fmt,
                                          int(bool(hadamard) and not plain), _ptr(h), _ptr(y), _ptr(codes),

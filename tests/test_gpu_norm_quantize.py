@@ -121,6 +121,16 @@ def test_empty_and_reused_buffers(ql):
     _check(ql, x, r, g, ql.QL_ROUTE_INT8, True, {key: None if key == "norm" else v[:6] for key, v in big.items()})
 
 
+def test_reused_buffers_of_a_plainer_call(ql):
+    """What the earlier result lacks (the sum, the norm) is made."""
+    x, r, g = (t.cuda() for t in _inputs(6, 1920, 15))
+    want = ql.qlinear_norm_quantize(x, g, ql.QL_ROUTE_INT8, residual=r, keep_norm=True)
+    bufs = ql.qlinear_norm_quantize(x, g, ql.QL_ROUTE_INT8)
+    q = ql.qlinear_norm_quantize(x, g, ql.QL_ROUTE_INT8, residual=r, keep_norm=True, out=bufs)
+    assert q["codes"] is bufs["codes"]
+    assert all(torch.equal(q[key], v) for key, v in want.items() if v is not None)
+
+
 @pytest.mark.parametrize("target", ["X", "residual"])
 def test_the_residual_stream_in_place(ql, target):
     x, r, g = _inputs(21, 1920, 12)
