@@ -38,8 +38,9 @@
 //               segment is stored row by row, so no row of another segment
 //               or behind the last one is written.
 //
-// What bounds a stage, and what that led to (17664 x 7680 x 1920 and, where
-// weights dominate, 32 experts x 192 rows x 1920 x 7680; B200):
+// What bounds a stage, and what that led to (eight experts, 17664 rows x 7680
+// x 1920, and, where weights dominate, 32 experts x 192 rows x 1920 x 7680;
+// each figure as measured at its step, B200):
 //   * the producers' issue: a TMA instruction costs its thread a hundred
 //     cycles or two.  One lane picked by elect.sync issues (behind `lane == 0`
 //     711 against 497 us at five per 64-deep stage), the weights come 256
@@ -50,12 +51,16 @@
 //     failed wait: 365 us; stages of two or four pieces with one commit for
 //     activations and A slot, see the next;
 //   * the slot's turn-around: MMA, commit, wait, widening, store.  Widening
-//     before the wait leaves only the store in it: 343 us, 1519 TFLOP/s
-//     (0.88 of the measured bf16 peak), and 144 us (165 before).
-// With few rows per expert the transform warps' instructions bound it
-// (conversions, f16x2 products and byte permutes all run at 64 lanes a cycle
-// and SM): 32 experts of 32 rows x 1920 x 7680 take 79 us against 41 for the
-// weights' bytes.
+//     before the wait leaves only the store in it: 343 us, and 144 us (165
+//     before).
+// Now: 349 to 359 us in different sessions (1450 to 1490 TFLOP/s, 0.85 to 0.87
+// of the measured bf16 peak), the tensor pipe active 75% of the time on a case
+// of 4416 rows.  Two sets of transform warps taking the stages in turn were
+// slower (359 against 383 us): the issue slots are half used already.
+// With few rows per expert the handshakes of a stage and the transform warps'
+// instructions bound it (conversions, f16x2 products and byte permutes all run
+// at 64 lanes a cycle and SM): 32 experts of 32 rows x 1920 x 7680 take 78 us
+// against 41 for the weights' bytes, 61 us with neither loads nor conversions.
 // All waits are bounded; on a timeout a role records it, drains its own
 // copies or MMAs and leaves the loop, and the CTA frees its tensor memory.
 #include "ql_common.cuh"
@@ -600,10 +605,9 @@ ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows
   }
   // Tile height by the rows per expert: a tall tile widens the weights once
   // for more rows, a low one leaves room for longer K stages and a deeper
-  // weight ring.  64 experts 1408 x 2048 at 32 / 64 / 128 rows each: 64-row
-  // tiles 36 / 51 / 70 us, 128-row 40 / 42 / 61, 192-row 48 / 49 / 54; 32
-  // experts 1920 x 7680 at 32 / 64 / 128: 79 / 97 / 164, 95 / 97 / 128,
-  // 121 / 123 / 131.
+  // weight ring.  64 experts 1408 x 2048 at 32 / 64 / 128 rows each on average:
+  // 64-row tiles 36 / 50 / 74 us, 128-row 43 / 46 / 59, 192-row 46 / 49 / 60;
+  // 32 experts 1920 x 7680: 78 / 97 / 164, 96 / 98 / 131, 110 / 113 / 129.
   if (T <= 40 * static_cast<int64_t>(w->E))
     return launch_grouped_cfg<64, 3, 4, 4>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
   if (T <= 100 * static_cast<int64_t>(w->E))

@@ -32,6 +32,18 @@
 // significant bits against the 8 of the bf16 output, and exact for an
 // unrotated block's bf16 values down to 2^-29 of its largest; the block's
 // sums are scaled back in fp32.
+//
+// A single row would fill one of the MMA's eight columns.  Its form lets
+// column c take scale block c's elements, so a block's eight sums come out
+// unscaled and are scaled in fp32: four products a tile and lane instead of 32
+// f16 pairs of weights.
+//
+// Measured (B200, weights from HBM): 1 x 15360 x 5120 bf16 rows 13.0 us (3.4
+// TB/s of weights; a copy's rate would be 6.9 us), 5 x 5120 x 13824 int8
+// 14.5 us, 1 x 1920 x 1920 4.0 us.  About 3.5 us of each is launch, first
+// loads and the sums; the rest is issue and latency of the widening, with 16
+// warps on an SM by registers (issue slots 39% active over the whole kernel,
+// top stalls: the loads' scoreboard, fixed latencies, the conversion pipe).
 #include <atomic>
 #include <type_traits>
 

@@ -15,7 +15,10 @@
 // row is split over threads (an fp32 sum would move the last bit of rstd and
 // with it codes next to a rounding border).
 //
-// Bound: HBM (7 to 10 bytes per element).  A row belongs to W warps; a thread
+// Bound: HBM (7 to 10 bytes per element) for bf16 output: 32760 x 5120 with a
+// residual 194.5 us, 6.9 TB/s.  The codes add the rotation, the maximum and the
+// rounding, and issue slots bound them (72% active): 17776 x 1920 to int8 47.3
+// us with a residual and the norm's output left out, 5.0 TB/s.  A row belongs to W warps; a thread
 // holds V vectors of 16 elements from the load to the codes, so the row is
 // read once and written once, and the only exchanges are two reductions over
 // the row.  In a 128-element Hadamard block (8 neighbouring threads) thread
@@ -108,9 +111,13 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
 // RN(x inv) + 1.5 2^23, whose low mantissa bits are rint(RN(x inv)) for a
 // product below 2^22 (here at most qmax + 1/2): full-rate adds where the
 // float-to-int conversion runs at an eighth of it.  The product is rounded by
-// itself (the _rn intrinsics are not contracted).
+// itself: a packed multiply and two single adds cannot be contracted.  (Packed
+// multiplies here and in the norm: 17776 x 1920 to int8 39.8 against 42.5 us.)
 constexpr float kRoundMagic = 12582912.0f;
-__device__ __forceinline__ float round_magic(float x, float inv) { return __fadd_rn(__fmul_rn(x, inv), kRoundMagic); }
+__device__ __forceinline__ float2 round_magic(float2 x, float inv) {
+  const float2 p = __fmul2_rn(x, make_float2(inv, inv));
+  return make_float2(__fadd_rn(p.x, kRoundMagic), __fadd_rn(p.y, kRoundMagic));
+}
 
 // Barrier of one row's warps.
 __device__ __forceinline__ void row_sync(int row_slot, int warps) {
@@ -208,9 +215,11 @@ __global__ void __launch_bounds__(kNormMaxThreads, V <= 2 ? 2 : 1) k_norm_quanti
         const uint32_t* gw = reinterpret_cast<const uint32_t*>(&g);
         uint32_t* yw = reinterpret_cast<uint32_t*>(&y[c]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          yw[i] = pack_bf16x2(__fmul_rn(__fmul_rn(bf16_lo(hw[i]), rstd), bf16_lo(gw[i])),
-                              __fmul_rn(__fmul_rn(bf16_hi(hw[i]), rstd), bf16_hi(gw[i])));
+        for (int i = 0; i < 4; ++i) {
+          const float2 n = __fmul2_rn(__fmul2_rn(make_float2(bf16_lo(hw[i]), bf16_hi(hw[i])), make_float2(rstd, rstd)),
+                                      make_float2(bf16_lo(gw[i]), bf16_hi(gw[i])));
+          yw[i] = pack_bf16x2(n.x, n.y);
+        }
       }
       if (active(v)) {
         const int64_t o = 2 * (base + offset(v));
@@ -251,7 +260,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, V <= 2 ? 2 : 1) k_norm_quanti
         const int64_t o = base + offset(v);
         float2 q[8];   // rounded codes plus the magic constant
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = make_float2(round_magic(P[v][j].x, inv), round_magic(P[v][j].y, inv));
+        for (int j = 0; j < 8; ++j) q[j] = round_magic(P[v][j], inv);
         if constexpr (OUT == kOutF16) {
           // the code itself (zero as +0), two per f16x2 convert (integers up to 127: exact)
           uint4 c[2];
@@ -289,7 +298,8 @@ ql_status launch_norm_quantize(const void* x, const void* residual, const void* 
   // Vectors per thread: two where rows fill the GPU and have the threads for
   // it (per row and warp the reductions, the root and the divisions cost as
   // much as a vector: 17776 x 1920 to int8 43.6 against 51.5 us, 17776 x 7680
-  // 165 against 244), one for few or short rows (one row of 5120: 3.0 us in
+  // 165 against 244 when this was chosen; four vectors up to 2048 elements 49
+  // against 47 with a residual), one for few or short rows (one row of 5120: 3.0 us in
   // 10 warps; 65536 x 256 42 against 65 us), four beyond 16384 elements.
   const bool one = K <= 16 * kNormMaxThreads && (K < 1024 || M < num_sms());
   const int V = one ? 1 : K <= 2 * 16 * kNormMaxThreads ? 2 : 4;
