@@ -26,6 +26,8 @@
 // warp cover whole 128-byte lines, distances 1, 2, 4 are packed f32x2
 // butterflies over the two chunks, 8, 16, 32 are lane exchanges and 64 is
 // inside a pair.
+#include <type_traits>
+
 #include "ql_common.cuh"
 #include "gemm_common.cuh"
 #include "launchers.h"
@@ -35,6 +37,7 @@ namespace ql {
 namespace {
 
 constexpr int kNormMaxThreads = 512;
+constexpr int kNormThreads3 = 256;   // with three vectors per thread: 85 registers, three CTAs on an SM
 
 struct NormArgs {
   const uint8_t* x;
@@ -127,23 +130,25 @@ __device__ __forceinline__ void row_sync(int row_slot, int warps) {
 
 }  // namespace
 
-template <int V, int OUT>
-__global__ void __launch_bounds__(kNormMaxThreads, V <= 2 ? 2 : 1) k_norm_quantize(const NormArgs p) {
+// L lanes of a warp hold a row (32: whole warps, one or more).
+template <int V, int OUT, int L>
+__global__ void __launch_bounds__(V == 3 ? kNormThreads3 : kNormMaxThreads, V <= 2 ? 2 : V == 3 ? 3 : 1) k_norm_quantize(const NormArgs p) {
   __shared__ double s_sum[kNormMaxThreads / 32];
   __shared__ float s_max[kNormMaxThreads / 32];
   const int warps = p.warps_per_row;             // blockDim.x / 32
   const uint32_t lane = lane_id();
-  const int slot = threadIdx.y;                  // row of this CTA
-  const int t = threadIdx.x;                     // thread within the row
-  const int warp = slot * warps + (t >> 5);
+  const int slot = threadIdx.y * (32 / L) + (L < 32 ? static_cast<int>(lane) / L : 0);   // row of this CTA
+  const int t = L < 32 ? static_cast<int>(lane) % L : threadIdx.x;                       // thread within the row
+  const int warp = threadIdx.y * warps + (threadIdx.x >> 5);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * p.rows_per_cta + slot;
   pdl_wait();
-  if (row < p.M) {                               // uniform over the row's warps
+  const bool live = row < p.M;                   // uniform over a row's warps
+  if (L < 32 ? __any_sync(0xffffffffu, live) : live) {
     const int64_t base = row * p.K;              // element offset of the row
     const int nvec = p.K >> 4;                   // 16-element vectors, a multiple of 8
     // element offset of this thread's first chunk of vector v; the second is 64 further
     auto offset = [&](int v) { return 128 * ((t + v * 32 * warps) >> 3) + 8 * (t & 7); };
-    auto active = [&](int v) { return t + v * 32 * warps < nvec; };
+    auto active = [&](int v) { return (L == 32 || live) && t + v * 32 * warps < nvec; };
     uint4 h[V][2];
     double sum = 0.0;
 #pragma unroll
@@ -193,8 +198,8 @@ __global__ void __launch_bounds__(kNormMaxThreads, V <= 2 ? 2 : 1) k_norm_quanti
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (warps > 1) {
+    for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (L == 32 && warps > 1) {
       if (lane == 0) s_sum[warp] = sum;
       row_sync(slot, warps);
       sum = 0.0;
@@ -244,8 +249,8 @@ __global__ void __launch_bounds__(kNormMaxThreads, V <= 2 ? 2 : 1) k_norm_quanti
     }
     if constexpr (OUT != kOutBf16) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (warps > 1) {
+      for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (L == 32 && warps > 1) {
         if (lane == 0) s_max[warp] = m;
         row_sync(slot, warps);
         m = 0.f;
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(kNormMaxThreads, V <= 2 ? 2 : 1) k_norm_quanti
       }
       const float fq = static_cast<float>(p.qmax);
       const float inv = (m == 0.f) ? 0.f : __fdiv_rn(fq, m);
-      if (t == 0) p.scales[row] = (m == 0.f) ? 0.f : __fdiv_rn(m, fq);
+      if (t == 0 && (L == 32 || live)) p.scales[row] = (m == 0.f) ? 0.f : __fdiv_rn(m, fq);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (!active(v)) continue;
@@ -295,14 +300,32 @@ ql_status launch_norm_quantize(const void* x, const void* residual, const void* 
                                float* scales, cudaStream_t st) {
   if (M == 0) return QL_OK;
   if (K > 4 * 16 * kNormMaxThreads) return QL_ERR_UNSUPPORTED_SHAPE;
-  // Vectors per thread: two where rows fill the GPU and have the threads for
-  // it (per row and warp the reductions, the root and the divisions cost as
-  // much as a vector: 17776 x 1920 to int8 43.6 against 51.5 us, 17776 x 7680
-  // 165 against 244 when this was chosen; four vectors up to 2048 elements 49
-  // against 47 with a residual), one for few or short rows (one row of 5120: 3.0 us in
-  // 10 warps; 65536 x 256 42 against 65 us), four beyond 16384 elements.
-  const bool one = K <= 16 * kNormMaxThreads && (K < 1024 || M < num_sms());
-  const int V = one ? 1 : K <= 2 * 16 * kNormMaxThreads ? 2 : 4;
+  // Vectors per thread V, and with them the warps of a row.  Few rows: the
+  // smallest V whose warps still run together, about 20 on an SM (148 x 4096
+  // to int8, with a residual as all of these: 2.9 us at V = 1, 3.9 at 2, 4.5 at
+  // 3; 600 x 2304 5.3, 5.1, 5.8).  Many rows: a warp costs about as much for
+  // its part of the row's reductions, root and divisions as for a third of a
+  // vector, and idle lanes cost what busy ones do, so the least of
+  // warps (1 + 3 V): 17776 x 1024 30, 25, 32 us at V = 1, 2, 3, x 1536 49, 44,
+  // 36, x 1920 55, 47, 62, x 2560 91, 72, 66 (one vector is behind wherever a row
+  // needs two warps).  Four vectors have half the warps on an SM and only take
+  // rows that need them.
+  auto warps_for = [&](int V) { return (K / 16 + 32 * V - 1) / (32 * V); };
+  auto fits = [&](int V) { return warps_for(V) <= (V == 3 ? kNormThreads3 : kNormMaxThreads) / 32; };
+  int V = 4, least = INT32_MAX;
+  for (int v = 1; v <= 3; ++v) {
+    if (!fits(v)) continue;
+    if (v <= 2 && M * warps_for(v) <= 20ll * num_sms()) {
+      V = v;
+      break;
+    }
+    const int cost = warps_for(v) * (1 + 3 * v);
+    if (v == 1 && cost > 4) continue;
+    if (cost < least) {
+      least = cost;
+      V = v;
+    }
+  }
   NormArgs p{};
   p.x = static_cast<const uint8_t*>(x);
   p.residual = static_cast<const uint8_t*>(residual);
@@ -317,14 +340,22 @@ ql_status launch_norm_quantize(const void* x, const void* residual, const void* 
   p.qmax = qmax;
   p.eps = static_cast<double>(eps);
   p.k_inv = 1.0 / static_cast<double>(K);
-  p.warps_per_row = (K / 16 + 32 * V - 1) / (32 * V);
-  p.rows_per_cta = std::max(1, 8 / p.warps_per_row);   // short rows share a CTA of up to 8 warps
+  p.warps_per_row = warps_for(V);
+  const int L = K <= 128 ? 8 : K <= 256 ? 16 : 32;     // rows of 128 and 256 share a warp: 65536 x 128 to int8 10.5 us against 37.8
+  const int slots = std::max(1, 8 / p.warps_per_row);  // short rows share a CTA of up to 8 warps
+  p.rows_per_cta = slots * (32 / L);
   const int64_t grid = (M + p.rows_per_cta - 1) / p.rows_per_cta;
-  void (*kern)(NormArgs) = nullptr;
-  if (out_kind == kOutInt8) kern = V == 1 ? k_norm_quantize<1, kOutInt8> : V == 2 ? k_norm_quantize<2, kOutInt8> : k_norm_quantize<4, kOutInt8>;
-  if (out_kind == kOutF16) kern = V == 1 ? k_norm_quantize<1, kOutF16> : V == 2 ? k_norm_quantize<2, kOutF16> : k_norm_quantize<4, kOutF16>;
-  if (out_kind == kOutBf16) kern = V == 1 ? k_norm_quantize<1, kOutBf16> : V == 2 ? k_norm_quantize<2, kOutBf16> : k_norm_quantize<4, kOutBf16>;
-  if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(32 * p.warps_per_row, p.rows_per_cta), 0, st, 1, p) !=
+  auto pick = [&](auto out) -> void (*)(NormArgs) {
+    constexpr int OUT = decltype(out)::value;
+    if (L == 8) return k_norm_quantize<1, OUT, 8>;
+    if (L == 16) return k_norm_quantize<1, OUT, 16>;
+    return V == 1 ? k_norm_quantize<1, OUT, 32> : V == 2 ? k_norm_quantize<2, OUT, 32> : V == 3 ? k_norm_quantize<3, OUT, 32> : k_norm_quantize<4, OUT, 32>;
+  };
+  using std::integral_constant;
+  void (*kern)(NormArgs) = out_kind == kOutInt8  ? pick(integral_constant<int, kOutInt8>{})
+                           : out_kind == kOutF16 ? pick(integral_constant<int, kOutF16>{})
+                                                 : pick(integral_constant<int, kOutBf16>{});
+  if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(32 * p.warps_per_row, slots), 0, st, 1, p) !=
       cudaSuccess) {
     (void)cudaGetLastError();
     return QL_ERR_CUDA;

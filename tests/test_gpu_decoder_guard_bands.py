@@ -56,6 +56,11 @@ def test_norm_quantize(ql, m, k):
         g.check()
 
 
+@pytest.mark.parametrize("m,k", [(3001, 128), (3001, 256), (3001, 512), (3001, 896), (1501, 1920), (3001, 1408), (1001, 4608)])
+def test_norm_quantize_many_rows(ql, m, k):
+    test_norm_quantize(ql, m, k)
+
+
 @pytest.mark.parametrize("m", [1, 3, 8, 11, 16])
 @pytest.mark.parametrize("n,k", [(16, 128), (112, 256), (144, 1920), (1936, 640)])
 def test_gemv(ql, m, n, k):

@@ -68,6 +68,24 @@ def test_matches_the_oracle(ql, m, k, fmt_name, residual):
     assert ql.qlinear_device_status() == 0
 
 
+@pytest.mark.parametrize("fmt_name", ["QL_ROUTE_INT8", "QL_ACT_INT6_F16", "QL_ROUTE_BF16"])
+@pytest.mark.parametrize("k", [128, 256, 384, 512, 640, 1152, 1536, 1920, 2304, 4608, 8192, 9216, 13824, 16512])
+def test_many_rows_as_few(ql, k, fmt_name):
+    """A row's result does not depend on how many rows the call has (the
+    rows' split over lanes and warps does): rows of one call against the same
+    rows 41 at a time, bit for bit."""
+    fmt = getattr(ql, fmt_name)
+    m = 3001 if k <= 4608 else 1001
+    x, r, g = (t.cuda() for t in _inputs(m, k, 16))
+    norm = fmt != ql.QL_ROUTE_BF16
+    got = ql.qlinear_norm_quantize(x, g, fmt, residual=r, keep_norm=norm)
+    got = {key: v for key, v in got.items() if v is not None}
+    assert set(got) == ({"codes", "scales", "residual", "norm"} if norm else {"codes", "residual"})
+    for lo in range(0, m, 41):
+        part = ql.qlinear_norm_quantize(x[lo:lo + 41], g, fmt, residual=r[lo:lo + 41], keep_norm=norm)
+        assert all(torch.equal(v[lo:lo + 41], part[key]) for key, v in got.items())
+
+
 def test_norm_against_its_formula_in_64_bits(ql):
     m, k = 64, 1920
     x, r, g = _inputs(m, k, 5)
