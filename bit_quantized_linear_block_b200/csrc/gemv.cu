@@ -220,7 +220,7 @@ __device__ __forceinline__ float block_to_f16(const uint4 (&raw)[4], int hadamar
 // NT: tiles of 8 rows of `a` (1: up to 8 rows, 2: up to 16).  ONE: the form
 // for a single row (0 never, 1 always, 2 where a row tile has one row).
 template <int NT, int ACT, bool GROUPED, int ONE>
-__global__ void __launch_bounds__(32 * kGvMaxWarps, NT == 1 ? 2 : 1) k_gemv(const GvArgs p) {
+__global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 : 1) k_gemv(const GvArgs p) {
   constexpr int kTokens = 8 * NT;
   constexpr bool kScaled = ACT == kGvBf16;       // a factor per row and K block
   constexpr int kXBytes = gv_x_bytes(NT), kXZero = kXBytes - 16;   // a warp's rows of `a`, then 16 zero bytes
@@ -537,14 +537,15 @@ int gemv_units(int32_t N) {
   return 2 * (N / 128) + (r == 0 ? 0 : r > 16 ? 2 : 1);
 }
 
-// Warps of a kernel that an SM's registers hold.
+// Warps of a kernel that an SM's registers hold (a quarter of them for each
+// SM sub-partition).
 int warps_per_sm(const void* kern) {
   cudaFuncAttributes a;
   if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) {
     (void)cudaGetLastError();
     return 8;
   }
-  return 65536 / (32 * ((a.numRegs + 7) / 8 * 8));
+  return 4 * (16384 / (32 * ((a.numRegs + 7) / 8 * 8)));
 }
 
 // tiles: row tiles (grouped: the most that the experts' rows can make).
