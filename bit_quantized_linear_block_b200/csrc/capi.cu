@@ -706,17 +706,17 @@ ql_status qlinear_prepare_experts(const void* W, int32_t E, int32_t N, int32_t K
 }
 
 namespace {
-// At most one row for two experts, or few rows over few experts: the form that
-// streams the weights without tensor-memory tiles (us, that form / the tiles:
-// 64 experts 1408 x 2048 at 16 / 32 / 64 rows 14 / 17, 18 / 18, 31 / 28; 32
-// experts 1920 x 7680 at 8 / 16 / 32 rows 20 / 23, 35 / 42, 43 / 42; one
-// expert 1920 x 1920 at one row 5.4 / 9.6).
-bool grouped_few(int64_t T, int64_t E) { return 2 * T <= E || (T <= 16 && E <= 4); }
+// Which form runs is a matter of T and the shape only, so that the workspace's
+// size and a captured graph do not depend on the offsets: up to 512 rows (as
+// far as both were measured) the form whose estimate is lower.
+bool grouped_few(int64_t T, const ql_experts* w) {
+  return T <= 512 && grouped_few_ns(T, w->E, w->N, w->K) <= grouped_tiles_ns(T, w->E, w->N, w->K);
+}
 }  // namespace
 
 size_t qlinear_grouped_gemm_ws_bytes(int64_t T, const ql_experts* w, int32_t gathers) {
   if (T <= 0 || w == nullptr || check_m(T) != QL_OK || check_experts_shape(w->E, w->N, w->K) != QL_OK) return 0;
-  return gathers && !grouped_few(T, w->E) ? align256(static_cast<size_t>(T) * w->K * 2) : 0;
+  return gathers && !grouped_few(T, w) ? align256(static_cast<size_t>(T) * w->K * 2) : 0;
 }
 
 ql_status qlinear_grouped_gemm(int32_t act_fmt, const void* a_codes, const float* a_scales, int64_t rows_a,
@@ -738,7 +738,7 @@ ql_status qlinear_grouped_gemm(int32_t act_fmt, const void* a_codes, const float
   QL_TRY(device_ready());
   if (T == 0) return QL_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (grouped_few(T, w->E))
+  if (grouped_few(T, w))
     return launch_grouped_few(a_codes, a_scales, rows_a, row_index, offsets, T, w, Y, st);
   return launch_gemm_grouped(a_codes, a_scales, rows_a, row_index, offsets, T, w, Y, ws, st, status_word());
 }

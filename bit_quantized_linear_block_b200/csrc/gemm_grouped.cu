@@ -510,6 +510,12 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, H>::THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// The most row tiles of `per` rows that T rows of E experts can make.
+static int64_t most_tiles(int64_t T, int64_t E, int64_t per) {
+  const int64_t e = std::min(E, T);
+  return e + (T - e) / per;
+}
+
 template <int BMT, int RS, int WS, int H>
 static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                                     const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
@@ -551,8 +557,7 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   p.wait_limit = limits.wait_limit;
   p.status = status;
   // the most tiles that the rows can make
-  const int64_t e = std::min<int64_t>(w->E, T);
-  const int64_t tiles = (e + (T - e) / BMT) * p.tiles_n;
+  const int64_t tiles = most_tiles(T, w->E, BMT) * p.tiles_n;
   if (tiles > 0x7FFFFFFF - num_sms()) return QL_ERR_UNSUPPORTED_SHAPE;
   auto kern = k_gemm_grouped<BMT, RS, WS, H>;
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return QL_ERR_CUDA;
@@ -567,9 +572,8 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
 // ---------------------------------------------------------------------------
 // Source rows into output order: out[r] = a[rows[r]] (zeros for a row that
 // does not exist).  HBM: 2 bytes per value written, and read where a row is
-// new to L2.  The product then loads whole
-// boxes; gathering inside it was slower, since each row tile is loaded once
-// per 128 columns of Y: 17664 x 7680 x 1920 took 974 us with four-row TMA
+// new to L2.  The product then loads whole boxes; gathering inside it was
+// slower, since each row tile is loaded once per 128 columns of Y: 17664 x 7680 x 1920 took 974 us with four-row TMA
 // gathers and 742 us with 16-byte asynchronous copies, against 388 us for
 // rows in order.
 // ---------------------------------------------------------------------------
@@ -589,6 +593,26 @@ __global__ void __launch_bounds__(kThreadsHbm) k_gather_rows(const uint4* a, con
   pdl_release();
 }
 
+// Tile height by the rows per expert: a tall tile widens the weights once
+// for more rows, a low one leaves room for longer K stages and a deeper
+// weight ring.  64 experts 1408 x 2048 at 32 / 64 / 128 rows each on average:
+// 64-row tiles 36 / 50 / 74 us, 128-row 43 / 46 / 59, 192-row 46 / 49 / 60;
+// 32 experts 1920 x 7680: 78 / 97 / 164, 96 / 98 / 131, 110 / 113 / 129.
+// Low tiles too where all of them run at once: a K step of theirs takes 0.63 us
+// per 256 elements, one of the others 0.45 to 0.6 per 128.
+static int grouped_tile_rows(int64_t T, int64_t E, int64_t N) {
+  if (T <= 40 * E || most_tiles(T, E, 64) * ((N + 127) / 128) <= kEstimateSms) return 64;
+  return T <= 100 * E ? 128 : 192;
+}
+
+// ns of the tiles beyond the launch, from the fullest SM's tiles (fits single
+// waves of the shapes below within 20%).
+int64_t grouped_tiles_ns(int64_t T, int64_t E, int64_t N, int64_t K) {
+  const int rows = grouped_tile_rows(T, E, N);
+  const int64_t sm_tiles = (most_tiles(T, E, rows) * ((N + 127) / 128) + kEstimateSms - 1) / kEstimateSms;
+  return 4000 + sm_tiles * (rows == 64 ? (K + 255) / 256 * 630 : (K + 127) / 128 * 500);
+}
+
 ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                               const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, void* gathered,
                               cudaStream_t st, int* status) {
@@ -603,16 +627,11 @@ ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows
     }
     x = gathered;
   }
-  // Tile height by the rows per expert: a tall tile widens the weights once
-  // for more rows, a low one leaves room for longer K stages and a deeper
-  // weight ring.  64 experts 1408 x 2048 at 32 / 64 / 128 rows each on average:
-  // 64-row tiles 36 / 50 / 74 us, 128-row 43 / 46 / 59, 192-row 46 / 49 / 60;
-  // 32 experts 1920 x 7680: 78 / 97 / 164, 96 / 98 / 131, 110 / 113 / 129.
-  if (T <= 40 * static_cast<int64_t>(w->E))
-    return launch_grouped_cfg<64, 3, 4, 4>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
-  if (T <= 100 * static_cast<int64_t>(w->E))
-    return launch_grouped_cfg<128, 4, 3, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
-  return launch_grouped_cfg<192, 3, 2, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+  switch (grouped_tile_rows(T, w->E, w->N)) {
+    case 64: return launch_grouped_cfg<64, 3, 4, 4>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+    case 128: return launch_grouped_cfg<128, 4, 3, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+    default: return launch_grouped_cfg<192, 3, 2, 2>(x, a_scales, rows_a, rows, offsets, T, w, Y, st, status);
+  }
 }
 
 }  // namespace ql

@@ -96,6 +96,11 @@ def test_grouped_gemm(ql, counts, n, k):
     assert ql.qlinear_device_status() == 0
 
 
+@pytest.mark.parametrize("counts", [[40] * 13, [33, 95, 129, 64, 90, 127], [300, 1, 290]], ids=len)     # the tile heights
+def test_grouped_gemm_in_tiles(ql, counts):
+    test_grouped_gemm(ql, counts, 2064, 384)
+
+
 @pytest.mark.parametrize("tokens", [1, 4, 90])
 def test_a_block_of_dense_and_expert_layers(ql, tokens):
     """norm -> dense layer (few rows or tiles) -> residual + norm -> two expert

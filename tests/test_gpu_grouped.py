@@ -130,6 +130,25 @@ def test_ragged_segments(ql, counts, n, k):
     assert ql.qlinear_device_status() == 0
 
 
+@pytest.mark.parametrize("per", [40, 100, 1000])     # rows per expert up to which a tile height is taken
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{sum(c)}")
+def test_ragged_segments_in_tiles(ql, counts, per):
+    """The same segments where the call's size asks for tensor-memory tiles of
+    each height: experts without rows fill up, rows behind the last segment
+    too, and are left as they are."""
+    n, k = 1552, 640
+    first, T = 3, max(545, sum(counts) + 8)
+    counts = counts + [0] * max(0, -(-T // per) - len(counts))
+    w, _ = _experts(ql, len(counts), n, k, 24)
+    q = _tokens(ql, T // 2, k, 25)
+    rows = torch.randint(0, T // 2, (T,), generator=torch.Generator().manual_seed(T)).to(torch.int32).cuda()
+    y = torch.full((T, n), 0.25, dtype=torch.bfloat16, device="cuda")
+    off = _offsets(counts, first)
+    ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, off, w, rows=rows, Y=y)
+    _check(ql, q, off, w, y, rows)
+    assert ql.qlinear_device_status() == 0
+
+
 @pytest.mark.parametrize("hadamard", [False, True])
 @pytest.mark.parametrize("fmt_name", ["QL_ACT_INT8_F16", "QL_ACT_INT6_F16"])
 @pytest.mark.parametrize("tokens", [7, 300])
@@ -161,11 +180,11 @@ def test_offsets_and_rows_out_of_range(ql, total):
 
 
 @pytest.mark.parametrize("gather", [False, True])
-@pytest.mark.parametrize("counts", [[3, 0, 5], [20, 30, 40], [60, 0, 100], [200, 150, 250]])   # every form
+@pytest.mark.parametrize("counts", [[3, 0, 5], [60, 0, 100], [39] * 13, [90] * 6, [200, 150, 250]], ids=len)   # every form
 def test_a_bad_row_stays_alone(ql, counts, gather):
     """NaN and infinite codes in rows inside and behind the segments, and in
     row 0, which stands beside the rows that do not exist."""
-    w, _ = _experts(ql, 3, 48, 256, 20)
+    w, _ = _experts(ql, len(counts), 2064, 256, 20)
     T = sum(counts) + 6
     q = _tokens(ql, T, 256, 21)
     off = _offsets(counts, 2)
@@ -173,7 +192,7 @@ def test_a_bad_row_stays_alone(ql, counts, gather):
     if gather:
         rows = torch.randint(0, T, (T,), generator=torch.Generator().manual_seed(T)).to(torch.int32).cuda()
         rows[3::7] = -1
-    y = torch.full((T, 48), 0.25, dtype=torch.bfloat16, device="cuda")
+    y = torch.full((T, 2064), 0.25, dtype=torch.bfloat16, device="cuda")
     want = ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, off, w, rows=rows, Y=y.clone())
     bad = {key: v.clone() for key, v in q.items() if v is not None}
     hit = torch.tensor([0, 4, 5, T - 1], device="cuda")
@@ -264,9 +283,9 @@ def test_a_decoder_block_in_one_graph(ql, tokens):
     del graphs
 
 
-@pytest.mark.parametrize("counts", [[20, 30, 40], [60, 100, 80], [200, 150, 250]])    # the three tile heights
+@pytest.mark.parametrize("counts", [[40] * 13, [90] * 6, [200, 150, 250]], ids=len)    # the three tile heights
 def test_a_wait_that_runs_out_is_reported(ql, counts):
-    w, _ = _experts(ql, 3, 512, 1920, 16)
+    w, _ = _experts(ql, len(counts), 2048, 1920, 16)
     q = _tokens(ql, sum(counts), 1920, 17)
     off = _offsets(counts)
     for rows in (None, torch.arange(sum(counts), dtype=torch.int32, device="cuda")):
