@@ -38,12 +38,13 @@
 // unscaled and are scaled in fp32: four products a tile and lane instead of 32
 // f16 pairs of weights.
 //
-// Measured (B200, weights from HBM): 1 x 15360 x 5120 bf16 rows 13.0 us (3.4
-// TB/s of weights; a copy's rate would be 6.9 us), 5 x 5120 x 13824 int8
-// 14.5 us, 1 x 1920 x 1920 4.0 us.  About 3.5 us of each is launch, first
-// loads and the sums; the rest is issue and latency of the widening, with 16
-// warps on an SM by registers (issue slots 39% active over the whole kernel,
-// top stalls: the loads' scoreboard, fixed latencies, the conversion pipe).
+// Measured (B200, weights from HBM): 1 x 15360 x 5120 bf16 rows 12.6 us (3.5
+// TB/s of weights; a copy's rate would be 6.9 us), 8 rows 18.4, 16 rows 27.5
+// (20.3 of f16 codes); 5 x 5120 x 13824 int8 14.5 us; 1 x 1920 x 1920 3.9 us.
+// About 3.5 us of each is launch, first loads and the sums; the rest is issue
+// and latency of the widening, with 12 or 16 warps on an SM by registers (issue
+// slots 39% active over the whole single-row kernel, top stalls: the loads'
+// scoreboard, fixed latencies, the conversion pipe).
 #include <atomic>
 #include <type_traits>
 
@@ -63,7 +64,12 @@ constexpr int kGvCodeBytes = 8 * 512;       // 4 MMA tiles x 2 row halves x 32 l
 constexpr int kGvStage = kGvCodeBytes + 2 * 512;   // + the scales of both row halves
 constexpr int kGvMaxCluster = 8;
 
-constexpr int gv_x_bytes(int nt) { return nt * (2048 + 32) + 16; }   // f16 fragments, 8 factors a tile, a zero piece
+// Rows of `a` as f16: 16-byte piece p = 4 row + t of plane q holds elements 32 t
+// + 8 q .. + 7 of a row of the tile.  bf16 rows come out of their rotation two
+// to a lane, and 32 bytes between the pairs of rows keep its stores free of
+// bank conflicts.
+constexpr int gv_x_plane(bool scaled) { return 512 + (scaled ? 128 : 0); }
+constexpr int gv_x_bytes(int nt, bool scaled) { return nt * (4 * gv_x_plane(scaled) + 32) + 16 + (scaled ? 512 : 0); }
 
 enum GvAct { kGvBf16 = 0, kGvF16 = 1, kGvI8 = 2 };
 
@@ -118,6 +124,15 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// D = A (16 x 16, bf16) B (16 x 8, bf16)
+__device__ __forceinline__ void mma_bf16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t v) { return __half22float2(e4m3x2_to_f16(v)); }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
@@ -130,11 +145,10 @@ __device__ __forceinline__ void i8x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t
   hi = h2_bits(__hsub2(bits_h2(__byte_perm(u, 0x64646464u, 0x4342u)), off));
 }
 
-// This lane's 32 elements [32 t, 32 t + 32) of a 128-element block as 16
-// f16x2 words, t = lane % 4; for bf16 rows also the factor that undoes the
-// block's power-of-two scaling.  All lanes of the warp call it.
+// This lane's 32 codes [32 t, 32 t + 32) of a 128-element block as 16 f16x2
+// words, t = lane % 4.
 template <int ACT>
-__device__ __forceinline__ float block_to_f16(const uint4 (&raw)[4], int hadamard, uint32_t (&w)[16]) {
+__device__ __forceinline__ void codes_to_f16(const uint4 (&raw)[4], uint32_t (&w)[16]) {
   if constexpr (ACT == kGvF16) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -143,8 +157,7 @@ __device__ __forceinline__ float block_to_f16(const uint4 (&raw)[4], int hadamar
       w[4 * q + 2] = raw[q].z;
       w[4 * q + 3] = raw[q].w;
     }
-    return 1.f;
-  } else if constexpr (ACT == kGvI8) {
+  } else {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       i8x4_to_f16x4(raw[q].x, w[8 * q], w[8 * q + 1]);
@@ -152,66 +165,106 @@ __device__ __forceinline__ float block_to_f16(const uint4 (&raw)[4], int hadamar
       i8x4_to_f16x4(raw[q].z, w[8 * q + 4], w[8 * q + 5]);
       i8x4_to_f16x4(raw[q].w, w[8 * q + 6], w[8 * q + 7]);
     }
-    return 1.f;
-  } else {
-    float2 P[16];   // (x_j, x_{j + 16})
+  }
+}
+
+// The rotation of bf16 rows.  H_128 is H_16 over four bits of the element index
+// times H_8 over the other three.  Bits 0, 2, 5, 6 are one MMA's k index as the
+// rows lie in the lanes (k = 2 t + i0 + 8 i2: bits 5 and 6 are t, 0 and 2 the
+// place in a loaded 16-byte piece), so eight MMAs with +-1 do H_16 without an
+// exchange of lanes or an unpacked value, and leave the eight values of bits 1,
+// 3, 4 in one lane, two rows at a time, for packed butterflies.  8 MMAs and 48
+// packed operations for 8 rows in place of 128 and 64 lane exchanges: 8 x 15360
+// x 5120 18.4 us against 20.8, 16 rows 27.5 against 33.0.  Products are exact,
+// sums fp32.  Without a rotation A is the matching permutation.
+__device__ __forceinline__ void rotation_operand(int hadamard, uint32_t (&a)[4]) {
+  const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
+  const uint32_t s = ((g >> 1) & t & 1) ^ ((g >> 2) & (t >> 1) & 1);   // sign of bits 5 and 6
+  const uint32_t s2 = s ^ (g & 1);                                     // and of bit 2
+  auto pair = [](uint32_t lo, uint32_t hi) { return 0x3F803F80u ^ (lo << 15) ^ (hi << 31); };
+  a[0] = pair(s, s);
+  a[1] = pair(s, s ^ 1);        // row g + 8: bit 0
+  a[2] = pair(s2, s2);
+  a[3] = pair(s2, s2 ^ 1);
+  if (!hadamard) {
+    const uint32_t here = t == (g >> 1) ? 0x3F80u : 0u;
+    a[0] = (g & 1) ? 0u : here;
+    a[1] = (g & 1) ? 0u : here << 16;
+    a[2] = (g & 1) ? here : 0u;
+    a[3] = (g & 1) ? here << 16 : 0u;
+  }
+}
+
+// A K block of 8 rows, row `lane / 4` in its four lanes as loaded, rotated by
+// `a` (kept in shared memory between the blocks: four registers less), each row scaled by its power of two and rounded to f16, into the tile's
+// planes at `dst`; the factors that undo the scaling to `factor`.
+__device__ __forceinline__ void rotate_block(const uint4 (&raw)[4], const uint32_t (&a)[4], int hadamard, uint8_t* dst,
+                                             float* factor) {
+  const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
+  float2 P[4][2][2];   // [bits 3, 4][bit 1][bit 0] of rows 2 t and 2 t + 1
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t lo[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
-      const uint32_t hi[4] = {raw[q + 2].x, raw[q + 2].y, raw[q + 2].z, raw[q + 2].w};
+  for (int q = 0; q < 4; ++q) {
+    float d[4];
+    mma_bf16_zero(d, a, raw[q].x, raw[q].z);
+    P[q][0][0] = make_float2(d[0], d[1]);
+    P[q][0][1] = make_float2(d[2], d[3]);
+    mma_bf16_zero(d, a, raw[q].y, raw[q].w);
+    P[q][1][0] = make_float2(d[0], d[1]);
+    P[q][1][1] = make_float2(d[2], d[3]);
+  }
+  if (hadamard) {
+    auto butterfly = [](float2& x, float2& y) {
+      const float2 u = x, v = y;
+      x = __fadd2_rn(u, v);
+      y = __ffma2_rn(v, make_float2(-1.f, -1.f), u);
+    };
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        P[8 * q + 2 * i] = make_float2(bf16_lo(lo[i]), bf16_lo(hi[i]));
-        P[8 * q + 2 * i + 1] = make_float2(bf16_hi(lo[i]), bf16_hi(hi[i]));
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) butterfly(P[q][0][k], P[q][1][k]);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        butterfly(P[0][b][k], P[1][b][k]);
+        butterfly(P[2][b][k], P[3][b][k]);
+        butterfly(P[0][b][k], P[2][b][k]);
+        butterfly(P[1][b][k], P[3][b][k]);
       }
     }
-    if (hadamard) {   // distances 1..8 between pairs, 16 inside a pair, 32 and 64 across lanes
-      const float2 m1 = make_float2(-1.f, -1.f);
+  }
+  float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-      for (int s = 1; s < 16; s <<= 1) {
+  for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if ((j & s) == 0) {
-            const float2 a = P[j], b = P[j + s];
-            P[j] = __fadd2_rn(a, b);
-            P[j + s] = __ffma2_rn(b, m1, a);
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) P[j] = make_float2(__fadd_rn(P[j].x, P[j].y), __fsub_rn(P[j].x, P[j].y));
-#pragma unroll
-      for (int s = 1; s < 4; s <<= 1) {
-        const float sg = (lane_id() & s) ? -1.f : 1.f;
-        const float2 sg2 = make_float2(sg, sg);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float2 o;
-          o.x = __shfl_xor_sync(0xffffffffu, P[j].x, s);
-          o.y = __shfl_xor_sync(0xffffffffu, P[j].y, s);
-          P[j] = __ffma2_rn(P[j], sg2, o);
-        }
-      }
+    for (int b = 0; b < 2; ++b) {
+      m0 = fmax3(m0, fabsf(P[q][b][0].x), fabsf(P[q][b][1].x));
+      m1 = fmax3(m1, fabsf(P[q][b][0].y), fabsf(P[q][b][1].y));
     }
-    float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = fmax3(m, fabsf(P[j].x), fabsf(P[j].y));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    // 2^(141 - e) brings [2^(e - 127), 2^(e - 126)) to [2^14, 2^15); e >= 15
-    // keeps it and its inverse normal numbers (a smaller block only loses
-    // bits far below the fp32 sums)
-    const uint32_t e = max(__float_as_uint(m) >> 23, 15u);
-    const float mul = __uint_as_float((268u - e) << 23);
-    const float2 mul2 = make_float2(mul, mul);
+  for (int o = 4; o < 32; o <<= 1) {
+    m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+    m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+  }
+  // 2^(141 - e) brings [2^(e - 127), 2^(e - 126)) to [2^14, 2^15); e >= 15
+  // keeps it and its inverse normal numbers (a smaller block only loses
+  // bits far below the fp32 sums)
+  const uint32_t e0 = max(__float_as_uint(m0) >> 23, 15u), e1 = max(__float_as_uint(m1) >> 23, 15u);
+  const float2 mul = make_float2(__uint_as_float((268u - e0) << 23), __uint_as_float((268u - e1) << 23));
+  uint8_t* out = dst + t * 160 + (g >> 1) * 16 + (g & 1) * 8;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) P[j] = __fmul2_rn(P[j], mul2);
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w0[2], w1[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = h2_bits(__floats2half2_rn(P[2 * i].x, P[2 * i + 1].x));
-      w[8 + i] = h2_bits(__floats2half2_rn(P[2 * i].y, P[2 * i + 1].y));
+    for (int b = 0; b < 2; ++b) {
+      const float2 lo = __fmul2_rn(P[q][b][0], mul), hi = __fmul2_rn(P[q][b][1], mul);
+      w0[b] = h2_bits(__floats2half2_rn(lo.x, hi.x));
+      w1[b] = h2_bits(__floats2half2_rn(lo.y, hi.y));
     }
-    return __uint_as_float((e - 14u) << 23);
+    *reinterpret_cast<uint2*>(out + q * gv_x_plane(true)) = make_uint2(w0[0], w0[1]);
+    *reinterpret_cast<uint2*>(out + q * gv_x_plane(true) + 64) = make_uint2(w1[0], w1[1]);
+  }
+  if (g == 0) {
+    factor[2 * t] = __uint_as_float((e0 - 14u) << 23);
+    factor[2 * t + 1] = __uint_as_float((e1 - 14u) << 23);
   }
 }
 
@@ -223,7 +276,9 @@ template <int NT, int ACT, bool GROUPED, int ONE>
 __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 : 1) k_gemv(const GvArgs p) {
   constexpr int kTokens = 8 * NT;
   constexpr bool kScaled = ACT == kGvBf16;       // a factor per row and K block
-  constexpr int kXBytes = gv_x_bytes(NT), kXZero = kXBytes - 16;   // a warp's rows of `a`, then 16 zero bytes
+  constexpr int kPlane = gv_x_plane(kScaled);
+  constexpr int kXBytes = gv_x_bytes(NT, kScaled);
+  constexpr int kXZero = NT * (4 * kPlane + 32);   // a warp's rows of `a` and their factors, 16 zero bytes, the rotation's operand
   constexpr int kRaw = ACT == kGvI8 ? 2 : 4;     // 16-byte pieces of a lane's 32 elements
   extern __shared__ __align__(16) uint8_t smem[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
@@ -283,7 +338,7 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
                         static_cast<size_t>(16 * (unit & 1) + g) * 16;
   uint8_t* ring = smem + warp * (kGvDepth * kGvStage);
   uint8_t* xbuf = smem + warps * (kGvDepth * kGvStage) + warp * kXBytes;
-  float* xscale = reinterpret_cast<float*>(xbuf + NT * 2048);
+  float* xscale = reinterpret_cast<float*>(xbuf + NT * 4 * kPlane);
   if (lane == 0) *reinterpret_cast<uint4*>(xbuf + kXZero) = make_uint4(0, 0, 0, 0);   // read in place of rows that are not there
   // This lane's pieces of block 0, moved on by a block of this warp with each
   // issue.  Tiles past N copy tile 0 again (their sums are not stored).
@@ -348,18 +403,28 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[i][nt][c] = 0.f;
 
+  if constexpr (kScaled) {
+    uint32_t rot[4];
+    rotation_operand(p.hadamard, rot);
+    *reinterpret_cast<uint4*>(xbuf + kXZero + 16 + 16 * lane) = make_uint4(rot[0], rot[1], rot[2], rot[3]);
+  }
   if (nblk > 0) load_a(0);
   for (int j0 = 0; j0 < nblk; j0 += gb) {
     __syncwarp();                                // the previous batch has been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      uint32_t w[16];
-      const float f = block_to_f16<ACT>(raw[nt], p.hadamard, w);
+      if constexpr (kScaled) {
+        const uint4 r = lds128(xbuf + kXZero + 16 + 16 * lane);
+        const uint32_t rot[4] = {r.x, r.y, r.z, r.w};
+        rotate_block(raw[nt], rot, p.hadamard, xbuf + nt * 4 * kPlane, xscale + 8 * nt);
+      } else {
+        uint32_t w[16];
+        codes_to_f16<ACT>(raw[nt], w);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint4*>(xbuf + nt * 2048 + q * 512 + lane * 16) =
-            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-      if (kScaled && t == 0) xscale[8 * nt + g] = f;
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(xbuf + (4 * nt + q) * kPlane + lane * 16) =
+              make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      }
     }
     __syncwarp();
     if (j0 + gb < nblk) load_a(j0 + gb);
@@ -376,7 +441,8 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const bool mine = one ? g == 2 * t + (q >> 1) : g < m2;
-          const int at = nt * 2048 + q * 512 + (one ? 4 * b + t : b * m2 * 4 + lane) * 16;
+          const int piece = one ? 4 * b + t : b * m2 * 4 + lane;
+          const int at = (4 * nt + q) * kPlane + piece * 16 + (kScaled ? (piece >> 3) * 32 : 0);
           xf[nt][q] = lds128(xbuf + (mine ? at : kXZero));
         }
       const uint4 sa = lds128(slot + kGvCodeBytes), sb = lds128(slot + kGvCodeBytes + 512);
@@ -555,7 +621,7 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   const int64_t ctas = units * tiles;
   auto kern = k_gemv<NT, ACT, GROUPED, ONE>;
   auto smem_for = [&](int warps, int S) {
-    const int ring = warps * (kGvDepth * kGvStage + gv_x_bytes(NT));
+    const int ring = warps * (kGvDepth * kGvStage + gv_x_bytes(NT, ACT == kGvBf16));
     const int red = 8 * NT * (warps * (kGvRows + 1) + (S > 1 ? S * kGvRows : 0)) * 4;
     return std::max(ring, red);
   };
