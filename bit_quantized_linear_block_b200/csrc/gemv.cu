@@ -17,9 +17,9 @@
 //     9 half-KB pieces; the rows are 16 consecutive r % 32 of one 128-row
 //     scale atom and their three 32-row shifts, so that one 16-byte load of
 //     scales serves the four tiles;
-//   * a CTA (W warps) owns 64 rows, its warps the K blocks of its K range in
-//     turn; a cluster of S CTAs splits K further when the rows alone do not
-//     fill the GPU.  Partial sums are added in a fixed order (warps through
+//   * a CTA (4 to 8 warps) owns 64 rows, its warps the K blocks of its K range
+//     in turn; a cluster of S CTAs splits K further where that fills the GPU
+//     more evenly.  Partial sums are added in a fixed order (warps through
 //     shared memory, CTAs through distributed shared memory), so results do
 //     not depend on timing and need no workspace;
 //   * each lane copies the pieces it will read itself (cp.async, kGvDepth
@@ -40,7 +40,7 @@
 //
 // Measured (B200, weights from HBM): 1 x 15360 x 5120 bf16 rows 12.6 us (3.5
 // TB/s of weights; a copy's rate would be 6.9 us), 8 rows 18.4, 16 rows 27.5
-// (20.3 of f16 codes); 5 x 5120 x 13824 int8 14.5 us; 1 x 1920 x 1920 3.9 us.
+// (20.3 of f16 codes); 5 x 5120 x 13824 int8 13.9 us; 1 x 1920 x 1920 4.0 us.
 // About 3.5 us of each is launch, first loads and the sums; the rest is issue
 // and latency of the widening, with 12 or 16 warps on an SM by registers (issue
 // slots 39% active over the whole single-row kernel, top stalls: the loads'
@@ -603,15 +603,24 @@ int gemv_units(int32_t N) {
   return 2 * (N / 128) + (r == 0 ? 0 : r > 16 ? 2 : 1);
 }
 
-// Warps of a kernel that an SM's registers hold (a quarter of them for each
-// SM sub-partition).
-int warps_per_sm(const void* kern) {
-  cudaFuncAttributes a;
-  if (cudaFuncGetAttributes(&a, kern) != cudaSuccess) {
+// Clusters of S CTAs of a kernel that are resident at once, -1 for none.
+int max_clusters(const void* kern, int S, int warps, int smem) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(S * num_sms()));
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (!set_smem_attr(kern, smem) || cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
-    return 8;
+    return -1;
   }
-  return 4 * (16384 / (32 * ((a.numRegs + 7) / 8 * 8)));
+  return n > 0 ? n : -1;
 }
 
 // tiles: row tiles (grouped: the most that the experts' rows can make).
@@ -625,41 +634,48 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
     const int red = 8 * NT * (warps * (kGvRows + 1) + (S > 1 ? S * kGvRows : 0)) * 4;
     return std::max(ring, red);
   };
-  // Warps of a CTA: one K block each (four at least: they all add up the
-  // partial sums), as far as two CTAs (one, if that is all an SM gets) stay
-  // resident together: 16 rows x 15360 x 5120 took 19.5 us in one wave of 6
-  // warps a CTA and 24.2 in two of 8.
-  static std::atomic<int> known{0};   // the same for every device
-  int reg_warps = known.load(std::memory_order_relaxed);
-  if (reg_warps == 0) known.store(reg_warps = warps_per_sm(reinterpret_cast<const void*>(kern)), std::memory_order_relaxed);
-  const int sms = num_sms();
-  auto sm_ctas = [&](int S) { return (ctas * S + sms - 1) / sms; };   // of the fullest SM
-  auto warps_for = [&](int S) {
-    const int64_t together = std::min<int64_t>(sm_ctas(S), 2);
-    int warps = std::max(4, std::min(kGvMaxWarps, (kb + S - 1) / S));
-    while (warps > 4 && (together * warps > reg_warps || together * (smem_for(warps, S) + 1024) > 227 * 1024)) --warps;
-    return warps;
+  auto resident = [&](int S, int warps) {   // CTAs that run at once
+    static std::atomic<int> known[kGvMaxCluster + 1][kGvMaxWarps + 1];   // the same for every device
+    int n = known[S][warps].load(std::memory_order_relaxed);
+    if (n == 0) {
+      n = max_clusters(reinterpret_cast<const void*>(kern), S, warps, smem_for(warps, S));
+      known[S][warps].store(n, std::memory_order_relaxed);
+    }
+    return static_cast<int64_t>(n) * S;
   };
-  // K split over S CTAs, all of them resident at once (clusters that had to
-  // wait for room were slow: 5120 x 13824 12.5 us at S = 3, 20 at 7): the
-  // least of 115 ns per K block of the fullest SM, 200 ns per block that a
-  // warp takes in turn and 500 ns for a cluster's barrier and hand-over,
-  // which fits the times of one int8 row within 10%: 1920 x 1920 4.1 us at
-  // S = 4 and 5.3 at 1, 7680 x 1920 5.4 at 1 and 5.6 at 4, 15360 x 5120 12.5
-  // at 1 and 13.1 at 2.
-  int S = 1;
+  // K split over S CTAs of a cluster, and the warps of a CTA, by the least of an
+  // estimate in ns, fitted to 108 layers and row counts at every split (its
+  // choices are 1.6 to 4% behind the best ones on average, S = 1 with eight
+  // warps 31%): the K blocks of the fullest SM, the turns that a warp takes, the
+  // cluster's barrier and hand-over, the warps of an SM, and the sums that a
+  // CTA's threads add up.  Clusters run together or not at all (2400 x 11904
+  // 12.5 us at S = 7, whose 38 clusters are one too many, against 8.2 at 6); from
+  // three CTAs on they do not fill every SM evenly.  Waves of single CTAs cost
+  // their start again.
+  constexpr bool kOne = !GROUPED && ONE == 1;
+  const int rows = GROUPED ? (NT == 1 ? 2 : 12) : p.M;   // of a row tile (grouped: unknown here)
+  const int sms = num_sms();
+  int S = 1, warps = 4;
   int64_t best = INT64_MAX;
   for (int s = 1; s <= kGvMaxCluster && (s == 1 || 2 * s <= kb); ++s) {
-    const int64_t per_cta = (kb + s - 1) / s, warps = warps_for(s);
-    if (s > 1 && sm_ctas(s) * warps > reg_warps) break;
-    const int64_t cost =
-        115 * sm_ctas(s) * per_cta + 200 * ((per_cta + warps - 1) / warps) + (s > 1 ? 500 : 0);
-    if (cost < best) {
-      best = cost;
-      S = s;
+    if (s == 7) continue;   // fits the fewest CTAs
+    const int64_t room = s < 3 ? sms : sms - 8, sm_ctas = (ctas * s + room - 1) / room;
+    const int per_cta = (kb + s - 1) / s;
+    for (int w : {4, 5, 6, 8}) {
+      int64_t cost = sm_ctas * per_cta * (kOne ? 90 : NT == 1 ? 130 : 200) +
+                     (per_cta + w - 1) / w * (ACT == kGvBf16 && !kOne ? 700 : 330) +
+                     (s == 1 ? 0 : kOne ? 900 : 1450) + sm_ctas * w * (NT == 1 ? 130 : 220) + 700 * rows / w;
+      if (cost >= best) continue;
+      const int64_t run = resident(s, w);
+      if (s > 1 && ctas * s > run) continue;
+      if (s == 1 && run > 0) cost += (ctas - 1) / run * 2000;
+      if (cost < best) {
+        best = cost;
+        S = s;
+        warps = w;
+      }
     }
   }
-  const int warps = warps_for(S);
   if (ctas * S > 0x7FFFFFFF) return QL_ERR_UNSUPPORTED_SHAPE;
   p.cluster = S;
   p.units = units;
