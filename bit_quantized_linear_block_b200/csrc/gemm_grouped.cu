@@ -599,18 +599,17 @@ __global__ void __launch_bounds__(kThreadsHbm) k_gather_rows(const uint4* a, con
 // 64-row tiles 36 / 50 / 74 us, 128-row 43 / 46 / 59, 192-row 46 / 49 / 60;
 // 32 experts 1920 x 7680: 78 / 97 / 164, 96 / 98 / 131, 110 / 113 / 129.
 // Low tiles too where all of them run at once: a K step of theirs takes 0.63 us
-// per 256 elements, one of the others 0.45 to 0.6 per 128.
+// per 256 elements, one of the others 0.4 to 0.6 per 128.
 static int grouped_tile_rows(int64_t T, int64_t E, int64_t N) {
   if (T <= 40 * E || most_tiles(T, E, 64) * ((N + 127) / 128) <= kEstimateSms) return 64;
   return T <= 100 * E ? 128 : 192;
 }
 
-// ns of the tiles beyond the launch, from the fullest SM's tiles (fits single
-// waves of the shapes below within 20%).
+// ns of the tiles beyond the launch, from the fullest SM's tiles.
 int64_t grouped_tiles_ns(int64_t T, int64_t E, int64_t N, int64_t K) {
   const int rows = grouped_tile_rows(T, E, N);
   const int64_t sm_tiles = (most_tiles(T, E, rows) * ((N + 127) / 128) + kEstimateSms - 1) / kEstimateSms;
-  return 4000 + sm_tiles * (rows == 64 ? (K + 255) / 256 * 630 : (K + 127) / 128 * 500);
+  return 2000 + sm_tiles * (rows == 64 ? (K + 255) / 256 * 630 : (K + 127) / 128 * 400);
 }
 
 ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,

@@ -723,13 +723,12 @@ static int grouped_few_rows(int64_t T, int64_t E) { return T <= 8 * E ? 8 : 16; 
 
 // ns beyond the launch: the K blocks of the fullest SM at the best split of K
 // whose CTAs are resident together (16 warps an SM, 12 with 16-row tiles), each
-// 200 ns, 250 with 16-row tiles, and 2 us more for those.  Chosen by this
-// estimate against that of the tensor-memory tiles, 104 shapes of 1 to 512 rows,
-// 1 to 64 experts, 32 x 896 to 7680 x 1920, lose 0.2% to the better form on
-// average (always tiles 36%, always this form 15%); us, this form / tiles: one expert 160 x 2816 at
-// 256 rows 9.9 / 13.0, 1920 x 1920 at 64 rows 8.6 / 10.1 and at 256 22.9 / 11.6,
-// seven 288 x 5120 at 32 rows 9.3 / 16.5, 64 experts 1408 x 2048 at 16 / 64 rows
-// 13.0 / 16.9, 29.4 / 27.8.
+// 150 ns, 250 with 16-row tiles, and 1 us more for those.  Chosen by this
+// estimate against that of the tensor-memory tiles, 252 shapes of 1 to 512
+// rows, 1 to 64 experts, 32 x 896 to 7680 x 1920, lose 0.2% to the better form on
+// average (always tiles 32%, always this form 18%); us, this form / tiles: one
+// expert 160 x 2816 at 256 rows 9.9 / 13.0, 1920 x 1920 at 64 rows 8.6 / 10.1 and
+// at 256 22.9 / 11.6, seven 288 x 5120 at 32 rows 9.3 / 16.5.
 int64_t grouped_few_ns(int64_t T, int64_t E, int64_t N, int64_t K) {
   const int rows = grouped_few_rows(T, E);
   const int64_t e = std::min(E, T), ctas = gemv_units(static_cast<int32_t>(N)) * (e + (T - e) / rows), kb = K / 128;
@@ -739,7 +738,7 @@ int64_t grouped_few_ns(int64_t T, int64_t E, int64_t N, int64_t K) {
     if (s > 1 && sm_ctas * std::max<int64_t>(4, std::min<int64_t>(kGvMaxWarps, per_cta)) > (rows == 8 ? 16 : 12)) break;
     blocks = std::min(blocks, sm_ctas * per_cta);
   }
-  return rows == 8 ? 200 * blocks : 2000 + 250 * blocks;
+  return rows == 8 ? 150 * blocks : 1000 + 250 * blocks;
 }
 
 ql_status launch_grouped_few(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
