@@ -1,5 +1,9 @@
 """The quantized linear layer for few rows (qlinear_gemv) against the fp64
 product of the same packed weights, for every operand format."""
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -158,3 +162,37 @@ def test_on_a_side_stream_and_in_a_graph(ql):
         assert torch.equal(outs[i], want)
         inputs[i].zero_()
     del graphs
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls of the decoder operators are captured: what
+    a launch finds out once must be legal in a capture."""
+    code = """
+import torch
+from bit_quantized_linear_block_b200 import qlinear as ql
+x = torch.randn(300, 640, device="cuda").bfloat16()
+g = torch.ones(640, device="cuda", dtype=torch.bfloat16)
+w = ql.qlinear_prepare_weights((0.02 * torch.randn(1920, 640, device="cuda")).bfloat16())
+e = ql.qlinear_prepare_experts((0.02 * torch.randn(3, 1920, 640, device="cuda")).bfloat16())
+off = torch.tensor([0, 100, 180, 300], dtype=torch.int32, device="cuda")
+few = torch.tensor([0, 1, 1, 5], dtype=torch.int32, device="cuda")
+big = torch.randint(0, 300, (900,), device="cuda").to(torch.int32)
+off3 = torch.tensor([0, 300, 500, 900], dtype=torch.int32, device="cuda")
+def step():
+    q = ql.qlinear_norm_quantize(x, g, ql.QL_ACT_INT8_F16, residual=x)
+    five = dict(codes=q["codes"][:5], scales=q["scales"][:5])
+    return [ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x), 1, w), ql.qlinear_gemv(ql.QL_ACT_INT8_F16, q, 16, w),
+            ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, five, few, e), ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, off, e),
+            ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, q, off3, e, rows=big)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and ql.qlinear_device_status() == 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
