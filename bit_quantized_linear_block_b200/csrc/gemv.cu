@@ -28,10 +28,14 @@
 // MMA operands are f16: a weight value E2M1 x E4M3 (at most 6 significant
 // bits, 2^-10 .. 2688) and an integer code are exact, products and sums are
 // fp32.  A bf16 row block (rotated or not) is scaled by a power of two that
-// brings its largest magnitude into [2^14, 2^15) and rounded to f16: 11
-// significant bits against the 8 of the bf16 output, and exact for an
-// unrotated block's bf16 values down to 2^-29 of its largest; the block's
-// sums are scaled back in fp32.
+// brings its largest magnitude into [2^14, 2^15); the block's sums are scaled
+// back in fp32.  Unrotated bf16 values are exact in f16 down to 2^-29 of the
+// block's largest.  Rotated ones are fp32 sums and take two f16 terms, the
+// value's rounding and the rounding of what is left, each with an MMA of its
+// own on the same widened weights: half a step of the second term is 2^-23 of
+// the value (2^-39 of the block's largest where that term is a subnormal f16).
+// One term would be off by up to 2^-11 of each value, and rows whose products
+// cancel would lose their result.
 //
 // A single row would fill one of the MMA's eight columns.  Its form lets
 // column c take scale block c's elements, so a block's eight sums come out
@@ -39,12 +43,13 @@
 // f16 pairs of weights.
 //
 // Measured (B200, weights from HBM): 1 x 15360 x 5120 bf16 rows 12.6 us (3.5
-// TB/s of weights; a copy's rate would be 6.9 us), 8 rows 18.4, 16 rows 27.5
-// (20.3 of f16 codes); 5 x 5120 x 13824 int8 13.9 us; 1 x 1920 x 1920 4.0 us.
+// TB/s of weights; a copy's rate would be 6.9 us), 8 rows 17.9, 16 rows 24.7;
+// to be rotated, in two terms: 14.8, 21.6, 32.9 (one term: 12.7, 18.6, 27.4);
+// 16 rows of f16 codes 20.5; 5 x 5120 x 13824 int8 13.9 us; 1 x 1920 x 1920 4.1 us.
 // About 3.5 us of each is launch, first loads and the sums; the rest is issue
-// and latency of the widening, with 12 or 16 warps on an SM by registers (issue
-// slots 39% active over the whole single-row kernel, top stalls: the loads'
-// scoreboard, fixed latencies, the conversion pipe).
+// and latency of the widening, with 8 to 16 warps on an SM by registers and
+// shared memory (issue slots 39% active over the whole single-row kernel with one
+// term, top stalls: the loads' scoreboard, fixed latencies, the conversion pipe).
 #include <atomic>
 #include <type_traits>
 
@@ -64,14 +69,18 @@ constexpr int kGvCodeBytes = 8 * 512;       // 4 MMA tiles x 2 row halves x 32 l
 constexpr int kGvStage = kGvCodeBytes + 2 * 512;   // + the scales of both row halves
 constexpr int kGvMaxCluster = 8;
 
-// Rows of `a` as f16: 16-byte piece p = 4 row + t of plane q holds elements 32 t
-// + 8 q .. + 7 of a row of the tile.  bf16 rows come out of their rotation two
-// to a lane, and 32 bytes between the pairs of rows keep its stores free of
-// bank conflicts.
-constexpr int gv_x_plane(bool scaled) { return 512 + (scaled ? 128 : 0); }
-constexpr int gv_x_bytes(int nt, bool scaled) { return nt * (4 * gv_x_plane(scaled) + 32) + 16 + (scaled ? 512 : 0); }
+enum GvAct { kGvBf16 = 0, kGvF16 = 1, kGvI8 = 2, kGvRotated = 3 };   // kGvRotated: bf16 rows to be rotated
+constexpr bool gv_scaled(int act) { return act == kGvBf16 || act == kGvRotated; }   // a factor per row and K block
+constexpr int gv_terms(int act) { return act == kGvRotated ? 2 : 1; }               // f16 terms of a value
 
-enum GvAct { kGvBf16 = 0, kGvF16 = 1, kGvI8 = 2 };
+// Rows of `a` as f16: 16-byte piece p = 4 row + t of plane q holds elements 32 t
+// + 8 q .. + 7 of a row of the tile; the planes of the second terms follow those
+// of all tiles' first.  bf16 rows come out of their rotation two to a lane, and
+// 32 bytes between the pairs of rows keep its stores free of bank conflicts.
+constexpr int gv_x_plane(int act) { return 512 + (gv_scaled(act) ? 128 : 0); }
+constexpr int gv_x_bytes(int nt, int act) {
+  return nt * (gv_terms(act) * 4 * gv_x_plane(act) + 32) + 16 + (gv_scaled(act) ? 512 : 0);
+}
 
 struct GvArgs {
   const uint8_t* a;          // rows [rows_a, K]
@@ -85,7 +94,7 @@ struct GvArgs {
   int64_t rows_a, rows_y;
   size_t expert_codes, expert_sf;
   int32_t M, N, K, E;
-  int32_t hadamard, cluster, units;
+  int32_t cluster, units;
   float alpha_mul;
 };
 
@@ -174,10 +183,12 @@ __device__ __forceinline__ void codes_to_f16(const uint4 (&raw)[4], uint32_t (&w
 // place in a loaded 16-byte piece), so eight MMAs with +-1 do H_16 without an
 // exchange of lanes or an unpacked value, and leave the eight values of bits 1,
 // 3, 4 in one lane, two rows at a time, for packed butterflies.  8 MMAs and 48
-// packed operations for 8 rows in place of 128 and 64 lane exchanges: 8 x 15360
-// x 5120 18.4 us against 20.8, 16 rows 27.5 against 33.0.  Products are exact,
-// sums fp32.  Without a rotation A is the matching permutation.
-__device__ __forceinline__ void rotation_operand(int hadamard, uint32_t (&a)[4]) {
+// packed operations for 8 rows in place of 128 and 64 lane exchanges: with one
+// term to a value, 8 x 15360 x 5120 took 18.4 us against 20.8, 16 rows 27.5
+// against 33.0.  Products are exact, sums fp32.  Without a rotation A is the
+// matching permutation.
+template <int ACT>
+__device__ __forceinline__ void rotation_operand(uint32_t (&a)[4]) {
   const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
   const uint32_t s = ((g >> 1) & t & 1) ^ ((g >> 2) & (t >> 1) & 1);   // sign of bits 5 and 6
   const uint32_t s2 = s ^ (g & 1);                                     // and of bit 2
@@ -186,7 +197,7 @@ __device__ __forceinline__ void rotation_operand(int hadamard, uint32_t (&a)[4])
   a[1] = pair(s, s ^ 1);        // row g + 8: bit 0
   a[2] = pair(s2, s2);
   a[3] = pair(s2, s2 ^ 1);
-  if (!hadamard) {
+  if constexpr (ACT == kGvBf16) {
     const uint32_t here = t == (g >> 1) ? 0x3F80u : 0u;
     a[0] = (g & 1) ? 0u : here;
     a[1] = (g & 1) ? 0u : here << 16;
@@ -196,9 +207,12 @@ __device__ __forceinline__ void rotation_operand(int hadamard, uint32_t (&a)[4])
 }
 
 // A K block of 8 rows, row `lane / 4` in its four lanes as loaded, rotated by
-// `a` (kept in shared memory between the blocks: four registers less), each row scaled by its power of two and rounded to f16, into the tile's
-// planes at `dst`; the factors that undo the scaling to `factor`.
-__device__ __forceinline__ void rotate_block(const uint4 (&raw)[4], const uint32_t (&a)[4], int hadamard, uint8_t* dst,
+// `a` (kept in shared memory between the blocks: four registers less), each row
+// scaled by its power of two and rounded to f16, into the tile's planes at
+// `dst`; the second terms of rotated values `second` bytes behind; the factors
+// that undo the scaling to `factor`.
+template <int ACT>
+__device__ __forceinline__ void rotate_block(const uint4 (&raw)[4], const uint32_t (&a)[4], uint8_t* dst, int second,
                                              float* factor) {
   const int lane = static_cast<int>(lane_id()), g = lane >> 2, t = lane & 3;
   float2 P[4][2][2];   // [bits 3, 4][bit 1][bit 0] of rows 2 t and 2 t + 1
@@ -212,7 +226,7 @@ __device__ __forceinline__ void rotate_block(const uint4 (&raw)[4], const uint32
     P[q][1][0] = make_float2(d[0], d[1]);
     P[q][1][1] = make_float2(d[2], d[3]);
   }
-  if (hadamard) {
+  if constexpr (ACT == kGvRotated) {
     auto butterfly = [](float2& x, float2& y) {
       const float2 u = x, v = y;
       x = __fadd2_rn(u, v);
@@ -245,22 +259,32 @@ __device__ __forceinline__ void rotate_block(const uint4 (&raw)[4], const uint32
     m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
   }
   // 2^(141 - e) brings [2^(e - 127), 2^(e - 126)) to [2^14, 2^15); e >= 15
-  // keeps it and its inverse normal numbers (a smaller block only loses
-  // bits far below the fp32 sums)
+  // keeps it and its inverse normal numbers (a smaller block's values are
+  // multiples of 2^-133, 2^-7 when scaled: still exact in the two terms)
   const uint32_t e0 = max(__float_as_uint(m0) >> 23, 15u), e1 = max(__float_as_uint(m1) >> 23, 15u);
   const float2 mul = make_float2(__uint_as_float((268u - e0) << 23), __uint_as_float((268u - e1) << 23));
   uint8_t* out = dst + t * 160 + (g >> 1) * 16 + (g & 1) * 8;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    uint32_t w0[2], w1[2];
+    uint32_t w0[2], w1[2], v0[2], v1[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const float2 lo = __fmul2_rn(P[q][b][0], mul), hi = __fmul2_rn(P[q][b][1], mul);
-      w0[b] = h2_bits(__floats2half2_rn(lo.x, hi.x));
-      w1[b] = h2_bits(__floats2half2_rn(lo.y, hi.y));
+      const __half2 r0 = __floats2half2_rn(lo.x, hi.x), r1 = __floats2half2_rn(lo.y, hi.y);
+      w0[b] = h2_bits(r0);
+      w1[b] = h2_bits(r1);
+      if constexpr (ACT == kGvRotated) {   // what the first term leaves, exact in fp32
+        const float2 f0 = __half22float2(r0), f1 = __half22float2(r1);
+        v0[b] = h2_bits(__floats2half2_rn(lo.x - f0.x, hi.x - f0.y));
+        v1[b] = h2_bits(__floats2half2_rn(lo.y - f1.x, hi.y - f1.y));
+      }
     }
-    *reinterpret_cast<uint2*>(out + q * gv_x_plane(true)) = make_uint2(w0[0], w0[1]);
-    *reinterpret_cast<uint2*>(out + q * gv_x_plane(true) + 64) = make_uint2(w1[0], w1[1]);
+    *reinterpret_cast<uint2*>(out + q * gv_x_plane(ACT)) = make_uint2(w0[0], w0[1]);
+    *reinterpret_cast<uint2*>(out + q * gv_x_plane(ACT) + 64) = make_uint2(w1[0], w1[1]);
+    if constexpr (ACT == kGvRotated) {
+      *reinterpret_cast<uint2*>(out + second + q * gv_x_plane(ACT)) = make_uint2(v0[0], v0[1]);
+      *reinterpret_cast<uint2*>(out + second + q * gv_x_plane(ACT) + 64) = make_uint2(v1[0], v1[1]);
+    }
   }
   if (g == 0) {
     factor[2 * t] = __uint_as_float((e0 - 14u) << 23);
@@ -270,15 +294,23 @@ __device__ __forceinline__ void rotate_block(const uint4 (&raw)[4], const uint32
 
 }  // namespace
 
+// The threads that the compiler makes registers for: 16 warps on an SM, 12 with
+// two row tiles or two terms, 8 with both (224 registers; at 12 warps it spills
+// 300 bytes: 16 x 15360 x 5120 42.5 against 36.7 us).
+constexpr int gv_max_threads(int nt, int act) { return (nt == 1) == (act == kGvRotated) ? 384 : 32 * kGvMaxWarps; }
+constexpr int gv_min_ctas(int nt, int act) { return nt == 1 && act != kGvRotated ? 2 : 1; }
+
 // NT: tiles of 8 rows of `a` (1: up to 8 rows, 2: up to 16).  ONE: the form
 // for a single row (0 never, 1 always, 2 where a row tile has one row).
 template <int NT, int ACT, bool GROUPED, int ONE>
-__global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 : 1) k_gemv(const GvArgs p) {
+__global__ void __launch_bounds__(gv_max_threads(NT, ACT), gv_min_ctas(NT, ACT)) k_gemv(const GvArgs p) {
   constexpr int kTokens = 8 * NT;
-  constexpr bool kScaled = ACT == kGvBf16;       // a factor per row and K block
-  constexpr int kPlane = gv_x_plane(kScaled);
-  constexpr int kXBytes = gv_x_bytes(NT, kScaled);
-  constexpr int kXZero = NT * (4 * kPlane + 32);   // a warp's rows of `a` and their factors, 16 zero bytes, the rotation's operand
+  constexpr bool kScaled = gv_scaled(ACT);
+  constexpr int kPlane = gv_x_plane(ACT);
+  constexpr int kXBytes = gv_x_bytes(NT, ACT);
+  constexpr int kSecond = NT * 4 * kPlane;       // from a first term to its second
+  constexpr int kXScale = gv_terms(ACT) * kSecond;
+  constexpr int kXZero = kXScale + NT * 32;      // a warp's rows of `a` and their factors, 16 zero bytes, the rotation's operand
   constexpr int kRaw = ACT == kGvI8 ? 2 : 4;     // 16-byte pieces of a lane's 32 elements
   extern __shared__ __align__(16) uint8_t smem[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
@@ -338,7 +370,7 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
                         static_cast<size_t>(16 * (unit & 1) + g) * 16;
   uint8_t* ring = smem + warp * (kGvDepth * kGvStage);
   uint8_t* xbuf = smem + warps * (kGvDepth * kGvStage) + warp * kXBytes;
-  float* xscale = reinterpret_cast<float*>(xbuf + NT * 4 * kPlane);
+  float* xscale = reinterpret_cast<float*>(xbuf + kXScale);
   if (lane == 0) *reinterpret_cast<uint4*>(xbuf + kXZero) = make_uint4(0, 0, 0, 0);   // read in place of rows that are not there
   // This lane's pieces of block 0, moved on by a block of this warp with each
   // issue.  Tiles past N copy tile 0 again (their sums are not stored).
@@ -405,7 +437,7 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
 
   if constexpr (kScaled) {
     uint32_t rot[4];
-    rotation_operand(p.hadamard, rot);
+    rotation_operand<ACT>(rot);
     *reinterpret_cast<uint4*>(xbuf + kXZero + 16 + 16 * lane) = make_uint4(rot[0], rot[1], rot[2], rot[3]);
   }
   if (nblk > 0) load_a(0);
@@ -416,7 +448,7 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
       if constexpr (kScaled) {
         const uint4 r = lds128(xbuf + kXZero + 16 + 16 * lane);
         const uint32_t rot[4] = {r.x, r.y, r.z, r.w};
-        rotate_block(raw[nt], rot, p.hadamard, xbuf + nt * 4 * kPlane, xscale + 8 * nt);
+        rotate_block<ACT>(raw[nt], rot, xbuf + nt * 4 * kPlane, kSecond, xscale + 8 * nt);
       } else {
         uint32_t w[16];
         codes_to_f16<ACT>(raw[nt], w);
@@ -435,16 +467,18 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
       const uint8_t* slot = ring + (j % kGvDepth) * kGvStage + 16 * lane;
       // B fragments: row g of the tile, elements 32 t + 8 q ..; for a single
       // row, column g takes scale block g's elements only
-      uint4 xf[NT][4];
+      auto x_piece = [&](int nt, int q, int second) {
+        const bool mine = one ? g == 2 * t + (q >> 1) : g < m2;
+        const int piece = one ? 4 * b + t : b * m2 * 4 + lane;
+        const int at = (4 * nt + q) * kPlane + piece * 16 + (kScaled ? (piece >> 3) * 32 : 0);
+        return lds128(xbuf + (mine ? at + second : kXZero));
+      };
+      uint4 xf[NT][4];   // two terms: loaded plane by plane, for registers
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bool mine = one ? g == 2 * t + (q >> 1) : g < m2;
-          const int piece = one ? 4 * b + t : b * m2 * 4 + lane;
-          const int at = (4 * nt + q) * kPlane + piece * 16 + (kScaled ? (piece >> 3) * 32 : 0);
-          xf[nt][q] = lds128(xbuf + (mine ? at : kXZero));
-        }
+        for (int q = 0; q < 4; ++q)
+          if constexpr (ACT != kGvRotated) xf[nt][q] = x_piece(nt, q, 0);
       const uint4 sa = lds128(slot + kGvCodeBytes), sb = lds128(slot + kGvCodeBytes + 512);
       const uint32_t sa4[4] = {sa.x, sa.y, sa.z, sa.w}, sb4[4] = {sb.x, sb.y, sb.z, sb.w};
       float f0[NT], f1[NT];
@@ -471,6 +505,11 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
         float part[4][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          uint4 xs{};   // the second terms
+          if constexpr (ACT == kGvRotated) {
+            xf[0][q] = x_piece(0, q, 0);
+            xs = x_piece(0, q, kSecond);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t ha[4], hb[4];
@@ -479,6 +518,10 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
             if (q == 0) mma_f16_zero(part[i], ha[0], hb[0], ha[1], hb[1], xf[0][q].x, xf[0][q].y);
             else mma_f16(part[i], ha[0], hb[0], ha[1], hb[1], xf[0][q].x, xf[0][q].y);
             mma_f16(part[i], ha[2], hb[2], ha[3], hb[3], xf[0][q].z, xf[0][q].w);
+            if constexpr (ACT == kGvRotated) {
+              mma_f16(part[i], ha[0], hb[0], ha[1], hb[1], xs.x, xs.y);
+              mma_f16(part[i], ha[2], hb[2], ha[3], hb[3], xs.z, xs.w);
+            }
           }
         }
 #pragma unroll
@@ -495,6 +538,14 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
       float part[4][NT][4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        uint4 xs[NT];   // the second terms
+        if constexpr (ACT == kGvRotated) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            xf[nt][q] = x_piece(nt, q, 0);
+            xs[nt] = x_piece(nt, q, kSecond);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // scales of elements 32 t .. 32 t + 31, one per 16; this q's as an f16 pair
@@ -515,6 +566,10 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
             if (kScaled && q == 0) mma_f16_zero(d, ha[0], hb[0], ha[1], hb[1], xf[nt][q].x, xf[nt][q].y);
             else mma_f16(d, ha[0], hb[0], ha[1], hb[1], xf[nt][q].x, xf[nt][q].y);
             mma_f16(d, ha[2], hb[2], ha[3], hb[3], xf[nt][q].z, xf[nt][q].w);
+            if constexpr (ACT == kGvRotated) {
+              mma_f16(d, ha[0], hb[0], ha[1], hb[1], xs[nt].x, xs[nt].y);
+              mma_f16(d, ha[2], hb[2], ha[3], hb[3], xs[nt].z, xs[nt].w);
+            }
           }
         }
       }
@@ -584,7 +639,7 @@ __global__ void __launch_bounds__(NT == 1 ? 32 * kGvMaxWarps : 384, NT == 1 ? 2 
       v = warps_sum(m, r);
     if (n < p.N) {
       float a = alpha;
-      if constexpr (ACT != kGvBf16) {
+      if constexpr (!kScaled) {
         int64_t src = row0 + m;
         if (GROUPED && p.rows != nullptr) src = p.rows[row0 + m];
         a = src >= 0 && src < p.rows_a ? __fmul_rn(alpha, ld_dep(p.a_scales + src)) : 0.f;
@@ -630,7 +685,7 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   const int64_t ctas = units * tiles;
   auto kern = k_gemv<NT, ACT, GROUPED, ONE>;
   auto smem_for = [&](int warps, int S) {
-    const int ring = warps * (kGvDepth * kGvStage + gv_x_bytes(NT, ACT == kGvBf16));
+    const int ring = warps * (kGvDepth * kGvStage + gv_x_bytes(NT, ACT));
     const int red = 8 * NT * (warps * (kGvRows + 1) + (S > 1 ? S * kGvRows : 0)) * 4;
     return std::max(ring, red);
   };
@@ -651,7 +706,10 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   // CTA's threads add up.  Clusters run together or not at all (2400 x 11904
   // 12.5 us at S = 7, whose 38 clusters are one too many, against 8.2 at 6); from
   // three CTAs on they do not fill every SM evenly.  Waves of single CTAs cost
-  // their start again.
+  // their start again, and with 8 warps on an SM more than that (16 rows of 15360
+  // x 5120 to be rotated: two waves of eight warps 36.7 us, one of four 32.8).
+  // The two-term form was added later: over 18 layers at 1, 3, 8 and 16 rows its
+  // choices are 1.1 to 2.4% behind.
   constexpr bool kOne = !GROUPED && ONE == 1;
   const int rows = GROUPED ? (NT == 1 ? 2 : 12) : p.M;   // of a row tile (grouped: unknown here)
   const int sms = num_sms();
@@ -663,12 +721,12 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
     const int per_cta = (kb + s - 1) / s;
     for (int w : {4, 5, 6, 8}) {
       int64_t cost = sm_ctas * per_cta * (kOne ? 90 : NT == 1 ? 130 : 200) +
-                     (per_cta + w - 1) / w * (ACT == kGvBf16 && !kOne ? 700 : 330) +
+                     (per_cta + w - 1) / w * (gv_scaled(ACT) && !kOne ? 700 : 330) +
                      (s == 1 ? 0 : kOne ? 900 : 1450) + sm_ctas * w * (NT == 1 ? 130 : 220) + 700 * rows / w;
       if (cost >= best) continue;
       const int64_t run = resident(s, w);
       if (s > 1 && ctas * s > run) continue;
-      if (s == 1 && run > 0) cost += (ctas - 1) / run * 2000;
+      if (s == 1 && run > 0) cost += (ctas - 1) / run * (NT == 2 && ACT == kGvRotated ? 6000 : 2000);
       if (cost < best) {
         best = cost;
         S = s;
@@ -704,11 +762,11 @@ ql_status launch_gemv(int act, const void* a, const float* a_scales, int64_t M, 
   p.M = static_cast<int32_t>(M);
   p.N = w->N;
   p.K = w->K;
-  p.hadamard = w->hadamard;
   p.alpha_mul = w->hadamard ? (1.0f / 128.0f) : 1.0f;
   auto by_act = [&](auto nt, auto one) {
     constexpr int NT = decltype(nt)::value, ONE = decltype(one)::value;
-    return act == 0   ? launch_gemv_cfg<NT, kGvBf16, false, ONE>(p, 1, st)
+    return act == 0 && w->hadamard ? launch_gemv_cfg<NT, kGvRotated, false, ONE>(p, 1, st)
+           : act == 0 ? launch_gemv_cfg<NT, kGvBf16, false, ONE>(p, 1, st)
            : act == 1 ? launch_gemv_cfg<NT, kGvF16, false, ONE>(p, 1, st)
                       : launch_gemv_cfg<NT, kGvI8, false, ONE>(p, 1, st);
   };

@@ -364,10 +364,12 @@ QL_API ql_status qlinear_gemm(int32_t act_fmt, const void* a_codes, const void* 
                        Y = bf16(g_w sum_k h[m,k] w[n,k]), h = H x and g_w / 128
                        when the weights are rotated.  (qlinear_gemm's
                        QL_ROUTE_BF16 multiplies the kept bf16 weights; this
-                       multiplies the packed ones.)  Each row's 128-element
-                       block of h is rounded to f16 after a power-of-two
-                       scaling: 2^-12 of a value that is not below 2^-29 of
-                       its block's largest.
+                       multiplies the packed ones.)  h is an fp32 sum, held
+                       as two f16 terms per value after a power-of-two scaling
+                       of each row's 128-element block: off by at most 2^-23
+                       of the value plus 2^-39 of its block's largest.
+                       Without a rotation a value is exact unless it is below
+                       2^-29 of its block's largest (then 2^-39 of that).
    Y must not overlap a.  A row with non-finite values affects no other row. */
 QL_API ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_scales, int64_t M,
                               const ql_weights* w, void* Y_bf16, void* stream);

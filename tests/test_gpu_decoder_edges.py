@@ -1,0 +1,106 @@
+"""The decoder-block operators where their precision or their rules could fail:
+rotated bf16 rows next to rounding borders and at the ends of the range, and
+rows beside others."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import decoder_oracle as D
+from oracle import qlinear_oracle as O
+from bit_quantized_linear_block_b200 import synthetic as S
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ql():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    from bit_quantized_linear_block_b200 import qlinear
+    return qlinear
+
+
+def _layer(ql, w, hadamard=True):
+    return (ql.qlinear_prepare_weights(w.cuda(), ql.QL_W_NVFP4, hadamard=hadamard),
+            O.prepare_weights_nvfp4(S.bf16_bits(w), hadamard))
+
+
+def _bf16_reference(x, wq, hadamard):
+    """The fp64 product r of bf16 rows and the bound of each output's error:
+    bf16 output rounding, 2^-8 of the value; fp32 sums, K/16 MMA steps for each
+    of two terms, K/128 block sums and 64 joins, each off by at most 2^-22 of
+    the absolute products' sum; and, when the rows are rotated, for each value
+    of a 128-element block two f16 terms (half a step of the second, 2^-23 of
+    the value; 2^-39 of the block's largest where that term is a subnormal
+    f16) and the rotation's own fp32 sums (one MMA step of 2^-22 and three
+    additions of 2^-24 of the block's absolute sum: under 2^-21 of it)."""
+    x = O.bf16_bits_to_f32(S.bf16_bits(x.cpu())).astype(np.float64)
+    m, k = x.shape
+    r = D.nvfp4_product(x, wq, hadamard)
+    z, dz = x, np.zeros_like(x)
+    if hadamard:
+        blocks = x.reshape(m, k // 128, 128)
+        z = blocks @ O.sylvester_hadamard(128).astype(np.float64)
+        dz = (2.0 ** -23 * np.abs(z) + 2.0 ** -39 * np.abs(z).max(-1, keepdims=True)
+              + 2.0 ** -21 * np.abs(blocks).sum(-1, keepdims=True)).reshape(m, k)
+        z = z.reshape(m, k)
+    w = np.abs(O.nvfp4_dequantize(wq["packed"], wq["sb"])).T * float(wq["g"]) / (128 if hadamard else 1)
+    steps = (k / 8 + k / 128 + 64) * 2.0 ** -22
+    inner = (np.abs(z) @ w) * steps + (dz @ w) * (1 + steps)
+    return r, 2.0 ** -8 * np.abs(r) + inner * (1 + 2.0 ** -8)
+
+
+def _check_bf16(x, wq, hadamard, y):
+    r, bound = _bf16_reference(x, wq, hadamard)
+    err = np.abs(y.double().cpu().numpy() - r)
+    assert np.isfinite(err).all() and (err <= bound).all(), float((err / np.maximum(bound, 1e-300)).max())
+    return r
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -60, 2.0 ** 90])
+@pytest.mark.parametrize("m", [1, 2, 5, 8, 11, 16])
+def test_rotated_rows_next_to_f16_borders(ql, m, scale):
+    """x = 1.5 at element 0 and 2^-11 at element b rotates to 1.5 + 2^-11 s, s
+    the signs of row b of H, every value half an f16 step from 1.5 and rounding
+    to it.  A weight row along s has the product 128 * 2^-11, all of it in what
+    that rounding drops."""
+    at = [1, 2, 3, 5, 7, 8, 16, 31, 32, 33, 64, 65, 96, 100, 126, 127]
+    w = torch.zeros(16, 256, dtype=torch.bfloat16)
+    w[range(16), at] = 0.5
+    w[range(16), [128 + b for b in at]] = 0.5
+    w, wq = _layer(ql, w)
+    x = torch.zeros(m, 256, dtype=torch.bfloat16)
+    for i in range(m):
+        x[i, 0], x[i, at[i]] = 1.5 * scale, 2.0 ** -11 * scale
+        x[i, 128], x[i, 128 + at[i]] = -3.0 * scale, 2.0 ** -10 * scale
+    z = (x[:, :128].double() @ torch.from_numpy(O.sylvester_hadamard(128)).double()).numpy() / scale
+    assert (z.astype(np.float16) == 1.5).all()
+    y = ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x.cuda()), m, w)
+    r = _check_bf16(x, wq, True, y)
+    assert (np.abs(r[range(m), range(m)]) > 2.0 ** -11 * scale).all()
+
+
+@pytest.mark.parametrize("m", [1, 4, 7, 16])
+@pytest.mark.parametrize("n,k", [(48, 128), (80, 1152), (64, 13824), (1920, 1920)])
+def test_rotated_rows_keep_two_terms(ql, n, k, m):
+    w, wq = _layer(ql, S.weights(n, k, 0.02, 31, n + k))
+    x = S.activations_fixed_outliers(m, k, max(1, k // 100), 30.0, m + k, 1)
+    _check_bf16(x, wq, True, ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x.cuda()), m, w))
+
+
+@pytest.mark.parametrize("hadamard", [False, True])
+@pytest.mark.parametrize("m", [1, 3, 12])
+def test_subnormal_rows(ql, m, hadamard):
+    """bf16 rows below 2^-126, whole and beside a block of ordinary values:
+    weights near 2^60 bring the output back among the normal numbers."""
+    n, k = 32, 384
+    gen = torch.Generator().manual_seed(m)
+    w, wq = _layer(ql, (torch.randn(n, k, generator=gen) * 2.0 ** 60).bfloat16(), hadamard)
+    x = (torch.randint(-127, 128, (m, k), generator=gen).double() * 2.0 ** -133).bfloat16()
+    x[0] = 2.0 ** -130
+    if m > 1:
+        x[1, 128:256] = torch.randn(128, generator=gen).bfloat16() * 2.0 ** -120
+        x[2, :128] = 0
+    y = ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x.cuda()), m, w)
+    assert bool((y.cpu()[0] != 0).any())
+    _check_bf16(x, wq, hadamard, y)
