@@ -257,8 +257,10 @@ __global__ void __launch_bounds__(V == 3 ? kNormThreads3 : kNormMaxThreads, V <=
         for (int w = 0; w < warps; ++w) m = fmaxf(m, s_max[slot * warps + w]);
       }
       const float fq = static_cast<float>(p.qmax);
-      const float inv = (m == 0.f) ? 0.f : __fdiv_rn(fq, m);
-      if (t == 0 && (L == 32 || live)) p.scales[row] = (m == 0.f) ? 0.f : __fdiv_rn(m, fq);
+      // a maximum so small that qmax over it is no fp32 number: the step 2^-128,
+      // a product with FLT_MAX and finite codes
+      const float inv = (m == 0.f) ? 0.f : fminf(__fdiv_rn(fq, m), 3.402823466e38f);
+      if (t == 0 && (L == 32 || live)) p.scales[row] = (m == 0.f) ? 0.f : fmaxf(__fdiv_rn(m, fq), 2.938735877e-39f);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (!active(v)) continue;

@@ -315,7 +315,8 @@ QL_API ql_status qlinear_quantize_act(const void* X_bf16, int64_t M, int32_t K,
      y = bf16(RN(RN(h rstd) gamma)),  rstd = RN(1 / sqrt(sum h^2 / K + eps))
          with the sum in fp64
      codes, scales = what qlinear_quantize_act gives for y in act_fmt, bit for
-         bit (in rows whose largest magnitude is 0 or at least 2^-120):
+         bit (in rows whose largest magnitude is 0 or at least 2^-120; a
+         smaller one has finite codes too, and a scale of at least 2^-128):
          QL_ROUTE_INT8, QL_ROUTE_INT6 (int8 [M, K] + fp32 [M]),
          QL_ACT_INT8_F16, QL_ACT_INT6_F16 (f16 [M, K] + fp32 [M]); or y itself
          for QL_ROUTE_BF16 (codes bf16 [M, K], scales unused, hadamard 0).

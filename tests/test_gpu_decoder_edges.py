@@ -104,3 +104,32 @@ def test_subnormal_rows(ql, m, hadamard):
     y = ql.qlinear_gemv(ql.QL_ROUTE_BF16, dict(codes=x.cuda()), m, w)
     assert bool((y.cpu()[0] != 0).any())
     _check_bf16(x, wq, hadamard, y)
+
+
+@pytest.mark.parametrize("k", [128, 256, 640, 4608, 16512])
+@pytest.mark.parametrize("fmt_name", ["QL_ROUTE_INT8", "QL_ACT_INT8_F16", "QL_ROUTE_INT6", "QL_ACT_INT6_F16"])
+def test_rows_whose_norm_is_tiny(ql, fmt_name, k):
+    """Rows whose largest magnitude is below qmax / FLT_MAX, so that qmax over it
+    is no fp32 number, beside a row of zeros: finite codes of the step 2^-128,
+    a subnormal fp32 number (amax / qmax is below it), within half a step of the
+    norm as it is returned, and FLT_MAX in place of 2^128 and the product's
+    rounding (2^-24 each of at most qmax steps).  fp32 sums of these norms are
+    exact: they are multiples of 2^-133 below 2^-120."""
+    fmt = getattr(ql, fmt_name)
+    qmax = 31 if fmt in (ql.QL_ROUTE_INT6, ql.QL_ACT_INT6_F16) else 127
+    gen = torch.Generator().manual_seed(k)
+    x = torch.randn(9, k, generator=gen).bfloat16().float()
+    x[:, 5::7] = 0
+    x[3] = 0
+    for hadamard in (False, True):
+        gamma = torch.full((k,), 2.0 ** (-131 if hadamard else -127)).bfloat16()
+        got = ql.qlinear_norm_quantize(x.bfloat16().cuda(), gamma.cuda(), fmt, hadamard=hadamard, keep_norm=True)
+        z = got["norm"].double()
+        if hadamard:
+            z = (z.view(9, -1, 128) @ torch.from_numpy(O.sylvester_hadamard(128)).double().cuda()).view(9, k)
+        amax = z.abs().amax(1)
+        assert bool((amax < qmax / 3.4e38).all()) and float(amax[0]) > 0
+        codes, scales = got["codes"].double(), got["scales"].double()
+        assert bool(torch.isfinite(codes).all()) and float(codes.abs().max()) <= qmax and bool((codes[0] != 0).any())
+        assert bool((scales == torch.where(amax > 0, 2.0 ** -128, 0.0)).all()) and bool((codes[3] == 0).all())
+        assert bool(((codes * 2.0 ** -128 - z).abs() <= 2.0 ** -128 * (0.5 + 2 * qmax * 2.0 ** -24)).all())
