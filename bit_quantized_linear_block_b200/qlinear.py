@@ -607,7 +607,8 @@ def qlinear_gemv(act_fmt: int, q: dict, M: int, w: PackedWeights, Y: torch.Tenso
     NVFP4 weights once.  `q`: qlinear_quantize_act's or qlinear_norm_quantize's
     dict for the per-token INT8 / INT6 formats; for QL_ROUTE_BF16
     {"codes": the unquantized bf16 input}, rotated here when the weights are,
-    against the packed weights."""
+    against the packed weights.  A row's bits do not depend on the other rows;
+    with another M its fp32 sums may run in another order."""
     _weights(w)
     M = int(M)
     if not 0 <= M <= GEMV_MAX_ROWS:
@@ -657,8 +658,8 @@ def qlinear_grouped_gemm(act_fmt: int, q: dict, offsets: torch.Tensor, w: Packed
     activations times expert e's weights.  `q`: the codes and scales of
     QL_ACT_INT8_F16 or QL_ACT_INT6_F16; `offsets`: int32 [E + 1]; `rows`:
     int32, one per row of Y (a token may appear in many rows).  Y has
-    Y.shape[0], rows.numel() or the codes' row count; its rows outside every
-    segment are left as they are (unset in a Y made here).  Offsets and rows
+    rows.numel() rows, without `rows` as many as the codes; its rows outside
+    every segment are left as they are (unset in a Y made here).  Offsets and rows
     stay on the device: no synchronization.  ws: scratch of
     lib.qlinear_grouped_gemm_ws_bytes(T, w.desc, rows is not None) bytes, made
     here when not given."""

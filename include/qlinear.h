@@ -371,7 +371,10 @@ QL_API ql_status qlinear_gemm(int32_t act_fmt, const void* a_codes, const void* 
                        of the value plus 2^-39 of its block's largest.
                        Without a rotation a value is exact unless it is below
                        2^-29 of its block's largest (then 2^-39 of that).
-   Y must not overlap a.  A row with non-finite values affects no other row. */
+   Y must not overlap a.  A row with non-finite values affects no other row.
+   For one M a row's bits depend on that row alone, not on its place or the
+   other rows.  Calls of another M may split K differently and add the fp32
+   sums in another order. */
 QL_API ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_scales, int64_t M,
                               const ql_weights* w, void* Y_bf16, void* stream);
 
@@ -396,9 +399,12 @@ QL_API ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_sca
    nearer end, and one below an earlier offset as that offset (an empty
    segment); a source row outside [0, rows_a) gives a row of zeros.  A row
    with non-finite values affects only the rows of Y that it is the source of.
-   Y must not overlap an operand.  4-byte aligned offsets and row_index.  ws: qlinear_grouped_gemm_ws_bytes(T,
-   w, row_index != NULL) bytes of scratch (0: ws may be NULL), 256-byte
-   aligned, not initialized; calls in flight at once need one each. */
+   T > 0 needs rows_a > 0.  The order of a row's fp32 sums follows T, the
+   weights' shape and how many rows its segment has, nothing else.  Y must not
+   overlap an operand.  offsets and row_index: 4-byte aligned.  ws:
+   qlinear_grouped_gemm_ws_bytes(T, w, row_index != NULL) bytes of scratch (0:
+   ws may be NULL), 256-byte aligned, not initialized; calls in flight at once
+   need one each. */
 QL_API size_t qlinear_experts_bytes(int32_t E, int32_t N, int32_t K);
 QL_API size_t qlinear_prepare_experts_ws_bytes(int32_t E, int32_t N, int32_t K);
 QL_API ql_status qlinear_prepare_experts(const void* W_bf16, int32_t E, int32_t N, int32_t K, int32_t hadamard,

@@ -133,3 +133,26 @@ def test_rows_whose_norm_is_tiny(ql, fmt_name, k):
         assert bool(torch.isfinite(codes).all()) and float(codes.abs().max()) <= qmax and bool((codes[0] != 0).any())
         assert bool((scales == torch.where(amax > 0, 2.0 ** -128, 0.0)).all()) and bool((codes[3] == 0).all())
         assert bool(((codes * 2.0 ** -128 - z).abs() <= 2.0 ** -128 * (0.5 + 2 * qmax * 2.0 ** -24)).all())
+
+
+@pytest.mark.parametrize("fmt_name", ["QL_ROUTE_BF16", "QL_ROUTE_INT8", "QL_ACT_INT8_F16"])
+@pytest.mark.parametrize("n,k", [(64, 13824), (2560, 1920)])
+@pytest.mark.parametrize("m", [2, 3, 6, 8, 9, 16])
+def test_rows_among_others_of_one_call_size(ql, m, n, k, fmt_name):
+    """For one M a row gives the same bits wherever it stands and whatever the
+    other rows hold.  (For another M the sums may run in another order: those
+    rows are held to the product in 64 bits.)"""
+    fmt = getattr(ql, fmt_name)
+    w = ql.qlinear_prepare_weights(S.weights(n, k, 0.02, 32, n).cuda(), ql.QL_W_NVFP4)
+    x = S.activations_fixed_outliers(m, k, max(1, k // 100), 30.0, m + k, 1).cuda()
+    q = dict(codes=x) if fmt == ql.QL_ROUTE_BF16 else ql.qlinear_quantize_act(x, fmt)
+    y = ql.qlinear_gemv(fmt, q, m, w)
+    turned = {key: v.roll(1, 0) for key, v in q.items() if v is not None and key in ("codes", "scales")}
+    assert torch.equal(ql.qlinear_gemv(fmt, turned, m, w), y.roll(1, 0))
+    other = {key: v.clone() for key, v in q.items() if v is not None and key in ("codes", "scales")}
+    if fmt == ql.QL_ROUTE_INT8:
+        other["codes"][1::2] = 127
+        other["scales"][1::2] = float("inf")
+    else:
+        other["codes"][1::2] = float("nan")
+    assert torch.equal(ql.qlinear_gemv(fmt, other, m, w)[::2], y[::2])
