@@ -510,12 +510,6 @@ __global__ void __launch_bounds__(GroupedCfg<BMT, RS, WS, H>::THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// The most row tiles of `per` rows that T rows of E experts can make.
-static int64_t most_tiles(int64_t T, int64_t E, int64_t per) {
-  const int64_t e = std::min(E, T);
-  return e + (T - e) / per;
-}
-
 template <int BMT, int RS, int WS, int H>
 static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                                     const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st,
@@ -557,7 +551,7 @@ static ql_status launch_grouped_cfg(const void* a, const float* a_scales, int64_
   p.wait_limit = limits.wait_limit;
   p.status = status;
   // the most tiles that the rows can make
-  const int64_t tiles = most_tiles(T, w->E, BMT) * p.tiles_n;
+  const int64_t tiles = most_row_tiles(T, w->E, BMT) * p.tiles_n;
   if (tiles > 0x7FFFFFFF - num_sms()) return QL_ERR_UNSUPPORTED_SHAPE;
   auto kern = k_gemm_grouped<BMT, RS, WS, H>;
   if (!set_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM)) return QL_ERR_CUDA;
@@ -601,14 +595,14 @@ __global__ void __launch_bounds__(kThreadsHbm) k_gather_rows(const uint4* a, con
 // Low tiles too where all of them run at once: a K step of theirs takes 0.63 us
 // per 256 elements, one of the others 0.4 to 0.6 per 128.
 static int grouped_tile_rows(int64_t T, int64_t E, int64_t N) {
-  if (T <= 40 * E || most_tiles(T, E, 64) * ((N + 127) / 128) <= kEstimateSms) return 64;
+  if (T <= 40 * E || most_row_tiles(T, E, 64) * ((N + 127) / 128) <= kEstimateSms) return 64;
   return T <= 100 * E ? 128 : 192;
 }
 
 // ns of the tiles beyond the launch, from the fullest SM's tiles.
 int64_t grouped_tiles_ns(int64_t T, int64_t E, int64_t N, int64_t K) {
   const int rows = grouped_tile_rows(T, E, N);
-  const int64_t sm_tiles = (most_tiles(T, E, rows) * ((N + 127) / 128) + kEstimateSms - 1) / kEstimateSms;
+  const int64_t sm_tiles = (most_row_tiles(T, E, rows) * ((N + 127) / 128) + kEstimateSms - 1) / kEstimateSms;
   return 2000 + sm_tiles * (rows == 64 ? (K + 255) / 256 * 630 : (K + 127) / 128 * 400);
 }
 

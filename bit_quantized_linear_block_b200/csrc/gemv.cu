@@ -658,6 +658,16 @@ int gemv_units(int32_t N) {
   return 2 * (N / 128) + (r == 0 ? 0 : r > 16 ? 2 : 1);
 }
 
+// CTAs that a split of K over S CTAs of a cluster is reckoned to run at once, one
+// to an SM; 0 for a split that is not tried.  From three CTAs on clusters do not
+// fill every SM (eight warps to a CTA: 296 CTAs are resident at S = 1 and 2, 264
+// to 284 at 3 to 8, but 259 at 7).  S = 7 was the best split of none of the 72
+// layers and row counts where it was measured.
+int64_t split_room(int S, int64_t k_blocks, int sms) {
+  if (S == 7 || (S > 1 && 2 * S > k_blocks)) return 0;
+  return S < 3 ? sms : sms - 8;
+}
+
 // Clusters of S CTAs of a kernel that are resident at once, -1 for none.
 int max_clusters(const void* kern, int S, int warps, int smem) {
   cudaLaunchConfig_t cfg{};
@@ -715,9 +725,10 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
   const int sms = num_sms();
   int S = 1, warps = 4;
   int64_t best = INT64_MAX;
-  for (int s = 1; s <= kGvMaxCluster && (s == 1 || 2 * s <= kb); ++s) {
-    if (s == 7) continue;   // fits the fewest CTAs
-    const int64_t room = s < 3 ? sms : sms - 8, sm_ctas = (ctas * s + room - 1) / room;
+  for (int s = 1; s <= kGvMaxCluster; ++s) {
+    const int64_t room = split_room(s, kb, sms);
+    if (room == 0) continue;
+    const int64_t sm_ctas = (ctas * s + room - 1) / room;
     const int per_cta = (kb + s - 1) / s;
     for (int w : {4, 5, 6, 8}) {
       int64_t cost = sm_ctas * per_cta * (kOne ? 90 : NT == 1 ? 130 : 200) +
@@ -789,10 +800,12 @@ static int grouped_few_rows(int64_t T, int64_t E) { return T <= 8 * E ? 8 : 16; 
 // at 256 22.9 / 11.6, seven 288 x 5120 at 32 rows 9.3 / 16.5.
 int64_t grouped_few_ns(int64_t T, int64_t E, int64_t N, int64_t K) {
   const int rows = grouped_few_rows(T, E);
-  const int64_t e = std::min(E, T), ctas = gemv_units(static_cast<int32_t>(N)) * (e + (T - e) / rows), kb = K / 128;
+  const int64_t ctas = gemv_units(static_cast<int32_t>(N)) * most_row_tiles(T, E, rows), kb = K / 128;
   int64_t blocks = INT64_MAX;
-  for (int s = 1; s <= kGvMaxCluster && (s == 1 || 2 * s <= kb); ++s) {
-    const int64_t sm_ctas = (ctas * s + kEstimateSms - 1) / kEstimateSms, per_cta = (kb + s - 1) / s;
+  for (int s = 1; s <= kGvMaxCluster; ++s) {
+    const int64_t room = split_room(s, kb, kEstimateSms);
+    if (room == 0) continue;
+    const int64_t sm_ctas = (ctas * s + room - 1) / room, per_cta = (kb + s - 1) / s;
     if (s > 1 && sm_ctas * std::max<int64_t>(4, std::min<int64_t>(kGvMaxWarps, per_cta)) > (rows == 8 ? 16 : 12)) break;
     blocks = std::min(blocks, sm_ctas * per_cta);
   }
@@ -818,12 +831,9 @@ ql_status launch_grouped_few(const void* a, const float* a_scales, int64_t rows_
   p.K = w->K;
   p.E = w->E;
   p.alpha_mul = w->hadamard ? (1.0f / 128.0f) : 1.0f;
-  auto tiles = [&](int64_t per) {   // sum of ceil(rows / per) over the experts, at most
-    const int64_t e = std::min<int64_t>(w->E, T);
-    return e + (T - e) / per;
-  };
-  return grouped_few_rows(T, w->E) == 8 ? launch_gemv_cfg<1, kGvF16, true, 2>(p, tiles(8), st)
-                                             : launch_gemv_cfg<2, kGvF16, true, 0>(p, tiles(16), st);
+  return grouped_few_rows(T, w->E) == 8
+             ? launch_gemv_cfg<1, kGvF16, true, 2>(p, most_row_tiles(T, w->E, 8), st)
+             : launch_gemv_cfg<2, kGvF16, true, 0>(p, most_row_tiles(T, w->E, 16), st);
 }
 
 }  // namespace ql

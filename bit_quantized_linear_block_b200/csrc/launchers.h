@@ -79,14 +79,20 @@ ql_status launch_gemv(int act, const void* a, const float* a_scales, int64_t M, 
 // The product grouped by expert for few rows per expert (f16 codes); rows may be null.
 ql_status launch_grouped_few(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                              const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, cudaStream_t st);
-// The same product on tensor-memory tiles; `gathered`: room for [T, K] f16
-// when rows is given.
+// The most row tiles of `per` rows that T rows of E experts can make: sum of
+// ceil(rows / per) over the experts, at most.
+inline int64_t most_row_tiles(int64_t T, int64_t E, int64_t per) {
+  const int64_t e = E < T ? E : T;
+  return e + (T - e) / per;
+}
 // Estimates of the two forms of the grouped product, in ns beyond the launch.
 // With a B200's SM count whatever the device, since a workspace may be sized
 // before there is one.
 constexpr int kEstimateSms = 148;
 int64_t grouped_few_ns(int64_t T, int64_t E, int64_t N, int64_t K);
 int64_t grouped_tiles_ns(int64_t T, int64_t E, int64_t N, int64_t K);
+// The same product on tensor-memory tiles; `gathered`: room for [T, K] f16
+// when rows is given.
 ql_status launch_gemm_grouped(const void* a, const float* a_scales, int64_t rows_a, const int32_t* rows,
                               const int32_t* offsets, int64_t T, const ql_experts* w, void* Y, void* gathered,
                               cudaStream_t st, int* status);

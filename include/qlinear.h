@@ -400,8 +400,8 @@ QL_API ql_status qlinear_gemv(int32_t act_fmt, const void* a, const float* a_sca
    segment); a source row outside [0, rows_a) gives a row of zeros.  A row
    with non-finite values affects only the rows of Y that it is the source of.
    T > 0 needs rows_a > 0.  The order of a row's fp32 sums follows T, the
-   weights' shape and how many rows its segment has, nothing else.  Y must not
-   overlap an operand.  offsets and row_index: 4-byte aligned.  ws:
+   weights' shape, how many rows its segment has and its place among them,
+   nothing else.  Y must not overlap an operand.  offsets and row_index: 4-byte aligned.  ws:
    qlinear_grouped_gemm_ws_bytes(T, w, row_index != NULL) bytes of scratch (0:
    ws may be NULL), 256-byte aligned, not initialized; calls in flight at once
    need one each. */
