@@ -668,7 +668,8 @@ int64_t split_room(int S, int64_t k_blocks, int sms) {
   return S < 3 ? sms : sms - 8;
 }
 
-// Clusters of S CTAs of a kernel that are resident at once, -1 for none.
+// Clusters of S CTAs of a kernel that are resident at once, -1 for none, 0 if
+// that cannot be found out now.
 int max_clusters(const void* kern, int S, int warps, int smem) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(S * num_sms()));
@@ -683,7 +684,7 @@ int max_clusters(const void* kern, int S, int warps, int smem) {
   int n = 0;
   if (!set_smem_attr(kern, smem) || cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
-    return -1;
+    return 0;
   }
   return n > 0 ? n : -1;
 }
@@ -704,7 +705,7 @@ ql_status launch_gemv_cfg(GvArgs p, int64_t tiles, cudaStream_t st) {
     int n = known[S][warps].load(std::memory_order_relaxed);
     if (n == 0) {
       n = max_clusters(reinterpret_cast<const void*>(kern), S, warps, smem_for(warps, S));
-      known[S][warps].store(n, std::memory_order_relaxed);
+      known[S][warps].store(n, std::memory_order_relaxed);   // 0: asked again by the next call
     }
     return static_cast<int64_t>(n) * S;
   };
