@@ -1,6 +1,7 @@
-"""The decoder-block operators where their precision or their rules could fail:
-rotated bf16 rows next to rounding borders and at the ends of the range, and
-rows beside others."""
+"""The decoder-block operators where their precision, their rules or their
+offsets could fail: rotated bf16 rows next to rounding borders and at the ends
+of the range, norms too small for their scale, rows beside others, every tile
+height of the grouped product, and more than 2^31 elements."""
 import numpy as np
 import pytest
 import torch
@@ -8,6 +9,7 @@ import torch
 from oracle import decoder_oracle as D
 from oracle import qlinear_oracle as O
 from bit_quantized_linear_block_b200 import synthetic as S
+from test_gpu_grouped import COUNTS, _check, _experts, _offsets, _tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -156,3 +158,84 @@ def test_rows_among_others_of_one_call_size(ql, m, n, k, fmt_name):
     else:
         other["codes"][1::2] = float("nan")
     assert torch.equal(ql.qlinear_gemv(fmt, other, m, w)[::2], y[::2])
+
+
+# fewest rows per expert that take tensor-memory tiles of this height, where the low tiles do not all run at once
+HEIGHTS = {64: 0, 128: 40, 192: 100}
+
+
+@pytest.mark.parametrize("height", HEIGHTS)
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{sum(c)}")
+def test_ragged_segments_at_each_tile_height(ql, counts, height):
+    """Every list of segments in a call whose rows, experts and columns ask for
+    tiles of this height: rows behind the last segment fill the call up and are
+    left as they are."""
+    n, k, first = 1552, 640, 3
+    counts = counts + [0] * max(0, 6 - len(counts))
+    e = len(counts)
+    T = max(545, sum(counts) + first + 5, HEIGHTS[height] * e + 1)
+    if height != 192:                         # experts without rows keep T / E low
+        e = max(e, -(-T // (40 if height == 64 else 100)))
+        counts = counts + [0] * (e - len(counts))
+    per = T / e
+    assert HEIGHTS[height] < per <= {64: 40, 128: 100, 192: T}[height]
+    assert (min(e, T) + (T - min(e, T)) // 64) * (-(-n // 128)) > 148
+    w, _ = _experts(ql, e, n, k, 33)
+    q = _tokens(ql, T // 2, k, 34)
+    rows = torch.randint(0, T // 2, (T,), generator=torch.Generator().manual_seed(T)).to(torch.int32).cuda()
+    off = _offsets(counts, first)
+    for r in (rows, None):
+        source = q if r is not None else _tokens(ql, T, k, 35)
+        y = torch.full((T, n), 0.25, dtype=torch.bfloat16, device="cuda")
+        ql.qlinear_grouped_gemm(ql.QL_ACT_INT8_F16, source, off, w, rows=r, Y=y)
+        _check(ql, source, off, w, y, r)
+    assert ql.qlinear_device_status() == 0
+
+
+def test_more_than_2_to_31_elements(ql):
+    """Inputs, outputs and weights whose element or byte offsets pass 2^31: the
+    last rows, columns and experts are those of a small call."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    f16 = ql.QL_ACT_INT8_F16
+    m, k = 160000, 13824                                       # norm: 2.2e9 elements
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, k, generator=gen, device="cuda").bfloat16()
+    g = torch.ones(k, dtype=torch.bfloat16, device="cuda")
+    q, want = ql.qlinear_norm_quantize(x, g, f16), ql.qlinear_norm_quantize(x[-3:].contiguous(), g, f16)
+    assert torch.equal(q["codes"][-3:], want["codes"]) and torch.equal(q["scales"][-3:], want["scales"])
+    assert bool((q["codes"][:2] == 0).all())
+    del x, q
+
+    T, n, k = 290000, 7680, 128                                # rows of Y: 2.2e9 elements
+    w, _ = _experts(ql, 2, n, k, 36)
+    q = _tokens(ql, 1000, k, 37)
+    rows = torch.randint(0, 1000, (T,), generator=gen, device="cuda").to(torch.int32)
+    off = torch.tensor([0, 5, T], dtype=torch.int32, device="cuda")
+    y = ql.qlinear_grouped_gemm(f16, q, off, w, rows=rows)
+    few = torch.tensor([0, 0, 600], dtype=torch.int32, device="cuda")
+    assert torch.equal(y[-600:], ql.qlinear_grouped_gemm(f16, q, few, w, rows=rows[-600:].contiguous()))
+    assert torch.equal(y[5:605], ql.qlinear_grouped_gemm(f16, q, few, w, rows=rows[5:605].contiguous()))
+    del y
+
+    e, n, k = 600, 7680, 1024                                  # experts: 4.7e9 weights, 2.4e9 bytes of codes
+    big = torch.zeros(e, n, k, dtype=torch.bfloat16, device="cuda")
+    big[-1] = 0.02 * torch.randn(n, k, generator=gen, device="cuda")
+    w, last = ql.qlinear_prepare_experts(big), ql.qlinear_prepare_experts(big[-1:].contiguous())
+    del big
+    for count in (9, 700):                                     # both forms
+        q = _tokens(ql, count, k, 38)
+        off = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
+        off[-1] = count
+        y = ql.qlinear_grouped_gemm(f16, q, off, w)
+        _check(ql, q, torch.tensor([0, count], dtype=torch.int32, device="cuda"), last, y)
+    del w
+
+    n, k = 1 << 17, 32768                                      # a layer: 4.3e9 weights
+    block = (0.02 * torch.randn(256, k, generator=gen, device="cuda")).bfloat16()
+    w, small = ql.qlinear_prepare_weights(block.repeat(n // 256, 1)), ql.qlinear_prepare_experts(block[None])
+    q = _tokens(ql, 3, k, 39)
+    y = ql.qlinear_gemv(f16, q, 3, w)
+    off = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    for at in (0, 256 * 255, n - 256):
+        _check(ql, q, off, small, y[:, at:at + 256].contiguous())
+    assert ql.qlinear_device_status() == 0
