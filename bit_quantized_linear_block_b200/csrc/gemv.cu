@@ -46,10 +46,13 @@
 // TB/s of weights; a copy's rate would be 6.9 us), 8 rows 17.9, 16 rows 24.7;
 // to be rotated, in two terms: 14.8, 21.6, 32.9 (one term: 12.7, 18.6, 27.4);
 // 16 rows of f16 codes 20.5; 5 x 5120 x 13824 int8 13.9 us; 1 x 1920 x 1920 4.1 us.
-// About 3.5 us of each is launch, first loads and the sums; the rest is issue
-// and latency of the widening, with 8 to 16 warps on an SM by registers and
-// shared memory (issue slots 39% active over the whole single-row kernel with one
-// term, top stalls: the loads' scoreboard, fixed latencies, the conversion pipe).
+// About 3.5 us of each is launch, first loads and the sums.  What is left bounds
+// differently: a single unrotated row takes 114 ns for each K block of the
+// fullest SM, against 106 at an SM's share of the copy rate, but 240 units on 148
+// SMs give that SM 80 K blocks where 64.9 is the average; 9 to 16 rows of codes
+// take 200 ns a block for the widening's issue and latencies, with 8 to 16 warps
+// on an SM by registers and shared memory (issue slots 33% active; two terms of 16
+// rows: 38%, tensor pipe 37%, fixed latencies the top stall).
 #include <atomic>
 #include <type_traits>
 
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(gv_max_threads(NT, ACT), gv_min_ctas(NT, ACT))
       }
       // All four tiles, step by step, so that their chains of dependent MMAs
       // overlap (a tile at a time, each waits for its own eight).  A tile past N
-      // multiplies what its ring slot happens to hold; nothing of it is stored.
+      // multiplies tile 0's weights again; nothing of it is stored.
       uint4 ca[4], cb[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
